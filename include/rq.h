@@ -69,6 +69,7 @@ typedef int32_t rq_status;
 #define RQ_INT8 6  /* symmetric INT8 (W4A8 / W8A8 settings): one byte per code in
                       -127..127, scale amax/127 per token (activations) or per
                       output channel (weight rows)                              */
+#define RQ_MXFP4 7 /* E2M1 nibbles + E8M0 block scale (a power of two) per 32    */
 
 /*
  * rq_make_rotation -- host.  Draw the RPBH rotation for K channels.
@@ -355,6 +356,91 @@ rq_status rq_w4a4_linear(int32_t a_fmt, int32_t w_fmt, int32_t M, int32_t N, int
 rq_status rq_w4a4_linear2(int32_t M, int32_t N, int32_t K, const uint8_t* a_codes, const float* a_scale,
                           const float* a_zero_point, const uint8_t* w_codes, const float* w_scale,
                           const float* w_zsum, void* Y, int32_t out_fp32, int32_t* status, void* stream);
+
+/*
+ * MXFP4 (RQ_MXFP4; OCP Microscaling Formats, MXFP4): blocks of 32 consecutive
+ * rotated coordinates, each an E2M1 nibble, times 2^(byte - 127).
+ *   amax = the block's largest |y| (y after the 1/sqrt(block) scaling);
+ *   byte = max(exponent bits of amax - 2, 0), so that the block's maximum
+ *   falls in [4, 8) on the E2M1 grid; element = e2m1(y 2^(127 - byte)), round
+ *   to nearest even, saturating at +-6.  A block with a NaN or an infinity
+ *   gets byte 255 (NaN) and zero codes: products with it are NaN.
+ * In the calls above RQ_MXFP4 is accepted by rq_rotate_quantize_act,
+ * rq_rotate_quantize_act2, rq_quantize_weights and rq_quantize_weights2
+ * (K % 64 == 0; K % 128 == 0 with U or rot2), and by rq_w4a4_linear as the pair
+ * (RQ_MXFP4, RQ_MXFP4), with or without the low-rank branch.  There are no row
+ * scales: `scale`, `a_scale` and `w_scale` are ignored and may be NULL.
+ *   block_scale: tiles of 128 rows x 128 columns, 512 bytes each, tile (mt, kt)
+ *          at (mt*ceil(K/128)+kt)*512, entry (m, kb = k/32) inside at
+ *          (m%32)*16 + ((m%128)/32)*4 + kb%4; size ceil(rows/128) *
+ *          ceil(K/128) * 512 bytes.  Padding entries are neither written nor
+ *          read as data.
+ *
+ * The calls below return RQ_OK for an empty batch (rows, M or T = 0) once
+ * their shapes are in order, whatever their pointers.
+ *
+ * rq_mxfp4_dequantize -- device, async.  The values that MXFP4 codes stand
+ * for: out [device, rows x K] FP32 (out_fp32 = 1) or BF16 (out_fp32 = 0; exact,
+ * but for magnitudes below 2^-126, which round).  K % 64 == 0.
+ */
+rq_status rq_mxfp4_dequantize(int32_t rows, int32_t K, const uint8_t* codes, const uint8_t* block_scale, void* out,
+                              int32_t out_fp32, void* stream);
+
+/*
+ * rq_mxfp4_layer -- device, async.  The whole MXFP4 linear layer from BF16
+ * rows: Y = Q(R X) W^T, the same results as rq_rotate_quantize_act followed by
+ * rq_w4a4_linear up to the order of the FP32 additions.
+ *   X [device, M x K] BF16; rot, block as rq_rotate_quantize_act; w_codes
+ *   [device, N x K/2], w_bscale from rq_quantize_weights(RQ_MXFP4, ...);
+ *   Y [device, M x N] FP32 or BF16 (out_fp32).  M >= 0, K % 64 == 0,
+ *   K <= 16384.
+ *   workspace [device] at least rq_mxfp4_layer_workspace(M, N, K) bytes, its
+ *   contents undefined before and after; calls that may overlap on the GPU
+ *   need one each.  That function returns -1 for a shape outside the limits.
+ */
+int64_t rq_mxfp4_layer_workspace(int32_t M, int32_t N, int32_t K);
+rq_status rq_mxfp4_layer(int32_t M, int32_t N, int32_t K, int32_t block, const uint16_t* X, const int32_t* rot,
+                         const uint8_t* w_codes, const uint8_t* w_bscale, void* workspace, int64_t workspace_bytes,
+                         void* Y, int32_t out_fp32, int32_t* status, void* stream);
+
+/*
+ * rq_mxfp4_moe -- device, async.  A mixture-of-experts layer on MXFP4 experts
+ * for a few tokens:
+ *   logits = X router^T (FP32 sums); the top_k largest of each token, largest
+ *   first, equal logits by the lower expert; weights = softmax over the chosen
+ *   logits (renorm = 1) or the chosen entries of the softmax over all E
+ *   (renorm = 0);
+ *   xq = Q(R x);  g = W1[e][0:I] xq,  u = W1[e][I:2I] xq;
+ *   h = weight * (g / (1 + exp(-g)) * u);  hq = Q(H h / sqrt(block2)) with H the
+ *   Walsh-Hadamard transform of each block2 hidden channels;
+ *   Y = sum over the token's experts of W2[e] hq.
+ * Q is MXFP4 in the FP32 order stated above.
+ *   X [device, T x K] BF16, 0 <= T <= RQ_MOE_MAX_TOKENS; router [device, E x K]
+ *   BF16, E <= RQ_MOE_MAX_EXPERTS; 1 <= top_k <= min(E, RQ_MOE_MAX_TOP_K).
+ *   rot, block: the rotation that W1's rows were quantized with.
+ *   w1_codes [device, E x 2I x K/2]: gate rows 0..I-1, up rows I..2I-1;
+ *   w1_bscale: E scale buffers of 2I rows each, one after another.
+ *   w2_codes [device, E x K x I/2], w2_bscale: E scale buffers of K rows, their
+ *   columns rotated with the plain block Hadamard of block2 channels (16, 32,
+ *   64 or 128).  A table with signs and a permutation is folded into W1
+ *   instead: give channel i of the gate row perm[i] and of the up row perm[i]
+ *   times its sign.
+ *   K % 64 == 0, K % block == 0, I % 128 == 0, both at most 16384.
+ *   topk_idx [device, T x top_k] int32 and topk_weight [device, T x top_k] FP32
+ *   out; Y [device, T x K] FP32 or BF16 (out_fp32).
+ *   workspace as rq_mxfp4_layer, rq_mxfp4_moe_workspace(...) bytes.
+ * A NaN logit ranks as -infinity: the chosen experts are always top_k
+ * different ones, and a token's NaN stays in its own row of Y.
+ */
+#define RQ_MOE_MAX_TOKENS 64
+#define RQ_MOE_MAX_EXPERTS 256
+#define RQ_MOE_MAX_TOP_K 16
+int64_t rq_mxfp4_moe_workspace(int32_t T, int32_t K, int32_t I, int32_t E, int32_t top_k);
+rq_status rq_mxfp4_moe(int32_t T, int32_t K, int32_t I, int32_t E, int32_t top_k, int32_t renorm, const uint16_t* X,
+                       const uint16_t* router, int32_t block, const int32_t* rot, const uint8_t* w1_codes,
+                       const uint8_t* w1_bscale, int32_t block2, const uint8_t* w2_codes, const uint8_t* w2_bscale,
+                       int32_t* topk_idx, float* topk_weight, void* workspace, int64_t workspace_bytes, void* Y,
+                       int32_t out_fp32, int32_t* status, void* stream);
 
 /*
  * rq_read_status -- synchronises `stream`, reads the device status word and

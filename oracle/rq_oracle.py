@@ -19,7 +19,8 @@ What it computes, in plain numpy, step by step as the pages state it:
   - a Lloyd-Max codebook for the known marginal of a rotated, normalised
     coordinate (OrbitQuant abstract),
   - NVFP4: e2m1 elements with 16-element e4m3 block scales (DiRotQ abstract:
-    NVFP4 on Blackwell);
+    NVFP4 on Blackwell),
+  - MXFP4: e2m1 elements with a power of two per 32 (OCP Microscaling Formats);
 * the DiRotQ low-rank branch: r PCA coefficients kept in BF16 and the residual
   quantized (DiRotQ abstract);
 * DiRotQ's full PCA rotation y = x V, its first r coordinates in BF16 and the
@@ -45,7 +46,7 @@ import math
 
 import numpy as np
 
-INT4, LM16, NVFP4, LM4, INT4A, INT8 = 1, 2, 3, 4, 5, 6
+INT4, LM16, NVFP4, LM4, INT4A, INT8, MXFP4 = 1, 2, 3, 4, 5, 6, 7
 
 MASK64 = (1 << 64) - 1
 F32 = np.float32
@@ -606,6 +607,45 @@ def quant_nvfp4(y: np.ndarray):
     return q.reshape(rows, K), sb, scale
 
 
+def quant_mxfp4(y: np.ndarray):
+    """MXFP4 (OCP Microscaling Formats: e2m1 elements, one E8M0 scale per 32,
+    exponent floor(log2 amax) - 2): byte = max(biased exponent of amax - 2, 0),
+    q = e2m1(y * 2^(127 - byte)), exact scaling.  A block with a NaN or an
+    infinity gets byte 255 and zero codes.
+    Returns (q nibble uint8 rows x K, byte uint8 rows x K/32).
+    Pinned by hand cases in tests/test_mxfp4.py."""
+    y = np.asarray(y, F32)
+    rows, K = y.shape
+    b = y.reshape(rows, K // 32, 32)
+    amax = np.max(np.abs(b), axis=2)          # NaN stays NaN
+    finite = np.isfinite(amax)
+    a64 = np.where(finite, amax, 1.0).astype(np.float64)
+    # frexp: a = m 2^e with 0.5 <= m < 1, so floor(log2 a) = e - 1
+    e = np.frexp(np.where(a64 > 0, a64, 1.0))[1] - 1
+    byte = np.where(a64 > 0, np.maximum(e - 2 + 127, 0), 0)
+    v = np.where(finite[:, :, None], b, 0).astype(np.float64) * np.exp2(127.0 - byte)[:, :, None]
+    q = _grid_round(v, E2M1_GRID).astype(np.uint8) | np.where(np.signbit(v), np.uint8(8), np.uint8(0))
+    q = np.where(finite[:, :, None], q, np.uint8(0))
+    return q.reshape(rows, K), np.where(finite, byte, 255).astype(np.uint8)
+
+
+def dequant_mxfp4(q: np.ndarray, byte: np.ndarray) -> np.ndarray:
+    """FP64 values of MXFP4 codes: e2m1 * 2^(byte - 127), NaN for byte 255."""
+    s = np.where(byte == 255, np.nan, np.exp2(np.asarray(byte, np.float64) - 127.0))
+    return e2m1_decode(q) * np.repeat(s, 32, axis=1)
+
+
+def route_top_k(logits: np.ndarray, top_k: int, renorm: bool):
+    """Expert choice from FP64 logits: the top_k largest per row, largest first,
+    equal ones by the lower index, NaN as -infinity; weights from the softmax
+    over the chosen (``renorm``) or over all."""
+    key = np.where(np.isnan(logits), -np.inf, logits)
+    idx = np.argsort(-key, axis=1, kind="stable")[:, :top_k]
+    p = np.exp(logits - np.max(key, axis=1, keepdims=True))
+    sel = np.take_along_axis(p, idx, axis=1)
+    return idx.astype(np.int32), sel / (sel if renorm else p).sum(axis=1, keepdims=True)
+
+
 # ----------------------------------------------------------------------------
 # Packing
 # ----------------------------------------------------------------------------
@@ -718,6 +758,9 @@ def rotate_quantize(x_bf16_f32: np.ndarray, fmt: int, block: int, sign, perm,
     elif fmt == NVFP4:
         q, sb, s = quant_nvfp4(y)
         out["q"], out["codes"], out["block_scale"], out["scale"] = q, pack_nibbles(q), sb, s
+    elif fmt == MXFP4:
+        q, sb = quant_mxfp4(y)
+        out["q"], out["codes"], out["block_scale"], out["scale"] = q, pack_nibbles(q), sb, None
     else:
         raise ValueError(fmt)
     return out
@@ -750,6 +793,8 @@ def dequant_values(q: np.ndarray, fmt: int, block_scale=None, centroids_e4m3=Non
         v = e2m1_decode(q)
         sb = e4m3_decode(block_scale)
         return v * np.repeat(sb, 16, axis=1)
+    if fmt == MXFP4:
+        return dequant_mxfp4(q, block_scale)
     raise ValueError(fmt)
 
 

@@ -58,7 +58,7 @@ rq_status check_rows_call(int32_t fmt, bool weight, const void* X, int32_t rows,
                           const int32_t* rot, const float* boundaries, const uint16_t* U, int32_t r,
                           const void* coef, const void* codes, const void* scale, const void* bscale,
                           const int32_t* rot2 = nullptr, const void* zp = nullptr) {
-  const bool fmt_ok = fmt == RQ_INT4 || fmt == RQ_LM16 || fmt == RQ_NVFP4 || fmt == RQ_INT8 ||
+  const bool fmt_ok = fmt == RQ_INT4 || fmt == RQ_LM16 || fmt == RQ_NVFP4 || fmt == RQ_INT8 || fmt == RQ_MXFP4 ||
                       (weight && fmt == RQ_LM4) || (!weight && fmt == RQ_INT4A);
   if (!fmt_ok) return fail(RQ_ERR_INVALID_ARG, "unknown or unsupported format %d", fmt);
   if (rows < 0 || K <= 0) return fail(RQ_ERR_INVALID_ARG, "bad shape rows=%d K=%d", rows, K);
@@ -68,10 +68,10 @@ rq_status check_rows_call(int32_t fmt, bool weight, const void* X, int32_t rows,
     return fail(RQ_ERR_UNSUPPORTED, "block %d with the low-rank branch: 128, 256 or 512", block);
   if (K % block) return fail(RQ_ERR_INVALID_ARG, "K=%d is not a multiple of block=%d", K, block);
   if (K > 16384) return fail(RQ_ERR_UNSUPPORTED, "K=%d exceeds 16384", K);
-  // codebook and NVFP4 rows need K % 64 (their packed rows stay whole 16-byte
+  // codebook, NVFP4 and MXFP4 rows need K % 64 (their packed rows stay whole 16-byte
   // units for the GEMM's tensor maps); INT4 groups, 8-bit codes, the low-rank
   // branch and the double rotation need K % 128
-  const bool k64 = (fmt == RQ_LM16 || fmt == RQ_LM4 || fmt == RQ_NVFP4) && !U && !rot2;
+  const bool k64 = (fmt == RQ_LM16 || fmt == RQ_LM4 || fmt == RQ_NVFP4 || fmt == RQ_MXFP4) && !U && !rot2;
   if (K % (k64 ? 64 : 128)) return fail(RQ_ERR_INVALID_ARG, "K=%d must be a multiple of %d", K, k64 ? 64 : 128);
   if (fmt == RQ_NVFP4 && U && K % 256) return fail(RQ_ERR_INVALID_ARG, "NVFP4 with the low-rank branch needs K %% 256 == 0 (K=%d)", K);
   if (rot2 && U) return fail(RQ_ERR_UNSUPPORTED, "the double rotation runs without the low-rank branch");
@@ -79,10 +79,12 @@ rq_status check_rows_call(int32_t fmt, bool weight, const void* X, int32_t rows,
   if (fmt == RQ_INT4A && !zp) return fail(RQ_ERR_INVALID_ARG, "asymmetric INT4 needs a zero-point output");
   if ((fmt == RQ_INT4A || fmt == RQ_INT8) && U) return fail(RQ_ERR_UNSUPPORTED, "format %d runs without the low-rank branch", fmt);
   if ((rot2 && !aligned16(rot2)) || (zp && !aligned16(zp))) return fail(RQ_ERR_ALIGNMENT, "rot2 / zero point not 16-byte aligned");
-  if (!X || !rot || !codes || !scale) return fail(RQ_ERR_INVALID_ARG, "null input/output pointer");
+  // MXFP4 has no row scales: `scale` is ignored
+  if (!X || !rot || !codes || (!scale && fmt != RQ_MXFP4)) return fail(RQ_ERR_INVALID_ARG, "null input/output pointer");
   if ((fmt == RQ_LM16 || fmt == RQ_LM4) && !boundaries)
     return fail(RQ_ERR_INVALID_ARG, "codebook format needs boundaries");
-  if (fmt == RQ_NVFP4 && !bscale) return fail(RQ_ERR_INVALID_ARG, "NVFP4 needs block_scale");
+  if ((fmt == RQ_NVFP4 || fmt == RQ_MXFP4) && !bscale)
+    return fail(RQ_ERR_INVALID_ARG, "%s needs block_scale", fmt == RQ_NVFP4 ? "NVFP4" : "MXFP4");
   if (U) {
     if (r < 8 || r > 32 || r % 8)
       return fail(RQ_ERR_UNSUPPORTED, "low-rank branch supports r in {8, 16, 24, 32} (got %d)", r);
@@ -327,17 +329,20 @@ static rq_status linear_impl(int32_t a_fmt, int32_t w_fmt, int32_t M, int32_t N,
   const bool pair_ok = (a_fmt == RQ_INT4 && w_fmt == RQ_INT4) || (a_fmt == RQ_INT4A && w_fmt == RQ_INT4) ||
                        (a_fmt == RQ_INT8 && w_fmt == RQ_INT4) || (a_fmt == RQ_INT8 && w_fmt == RQ_INT8) ||
                        (a_fmt == RQ_LM16 && w_fmt == RQ_LM16) ||
-                       (a_fmt == RQ_LM16 && w_fmt == RQ_LM4) || (a_fmt == RQ_NVFP4 && w_fmt == RQ_NVFP4);
+                       (a_fmt == RQ_LM16 && w_fmt == RQ_LM4) || (a_fmt == RQ_NVFP4 && w_fmt == RQ_NVFP4) ||
+                       (a_fmt == RQ_MXFP4 && w_fmt == RQ_MXFP4);
   if (!pair_ok) return fail(RQ_ERR_UNSUPPORTED, "format pair (%d, %d) not supported", a_fmt, w_fmt);
   if (M < 0 || N <= 0 || K <= 0) return fail(RQ_ERR_INVALID_ARG, "bad shape M=%d N=%d K=%d", M, N, K);
   if (w_fmt == RQ_INT4 && N % 4)   // the group scales of a tile are copied 16 bytes at a time
     return fail(RQ_ERR_INVALID_ARG, "INT4 weights need N %% 4 == 0 (N=%d)", N);
-  // codebook and NVFP4 codes: K % 64 (a ragged last K step issues only its
-  // MMAs inside K); INT4 and 8-bit weights: whole 128-wide groups
-  const bool k64 = a_fmt == RQ_LM16 || a_fmt == RQ_NVFP4;
+  // codebook, NVFP4 and MXFP4 codes: K % 64 (a ragged last K step issues only
+  // its MMAs inside K); INT4 and 8-bit weights: whole 128-wide groups
+  const bool k64 = a_fmt == RQ_LM16 || a_fmt == RQ_NVFP4 || a_fmt == RQ_MXFP4;
   if (K % (k64 ? 64 : 128)) return fail(RQ_ERR_INVALID_ARG, "K=%d must be a multiple of %d", K, k64 ? 64 : 128);
-  if (!a_codes || !a_scale || !w_codes || !w_scale || !Y) return fail(RQ_ERR_INVALID_ARG, "null pointer");
-  if (a_fmt == RQ_NVFP4 && (!a_bscale || !w_bscale)) return fail(RQ_ERR_INVALID_ARG, "NVFP4 needs block scales");
+  const bool mx = a_fmt == RQ_MXFP4;   // no row scales: a_scale and w_scale are ignored
+  if (!a_codes || !w_codes || !Y || (!mx && (!a_scale || !w_scale))) return fail(RQ_ERR_INVALID_ARG, "null pointer");
+  if ((mx || a_fmt == RQ_NVFP4) && (!a_bscale || !w_bscale))
+    return fail(RQ_ERR_INVALID_ARG, "%s needs block scales", mx ? "MXFP4" : "NVFP4");
   if (a_fmt == RQ_LM16 && (!a_lut || !w_lut)) return fail(RQ_ERR_INVALID_ARG, "codebook formats need LUTs");
   if ((c != nullptr) != (L != nullptr)) return fail(RQ_ERR_INVALID_ARG, "c and L must both be given or both NULL");
   // 16-level codes are stored sign-magnitude: the GEMM reads the upper half of
@@ -396,6 +401,113 @@ static rq_status linear_impl(int32_t a_fmt, int32_t w_fmt, int32_t M, int32_t N,
                                                        : rq::launch_gemm(g, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess)
     return fail(RQ_ERR_CUDA, "GEMM launch failed: %s%s%s", cudaGetErrorString(e), why ? " / " : "", why ? why : "");
+  return ok();
+}
+
+// ------------------------------------------------------------------ MXFP4
+static bool pow2(int32_t v) { return v > 0 && (v & (v - 1)) == 0; }
+static rq_status check_block(int32_t K, int32_t block) {
+  if (block < 16 || block > 1024 || !pow2(block))
+    return fail(RQ_ERR_UNSUPPORTED, "block %d: a power of two from 16 to 1024", block);
+  if (K % block) return fail(RQ_ERR_INVALID_ARG, "K=%d is not a multiple of block=%d", K, block);
+  if (K > 16384) return fail(RQ_ERR_UNSUPPORTED, "K=%d exceeds 16384", K);
+  return RQ_OK;
+}
+static int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
+static int64_t mx_tiles(int64_t rows, int64_t K) { return (rows + 127) / 128 * ((K + 127) / 128) * 512; }
+
+rq_status rq_mxfp4_dequantize(int32_t rows, int32_t K, const uint8_t* codes, const uint8_t* block_scale, void* out,
+                              int32_t out_fp32, void* stream) {
+  if (rows < 0 || K <= 0 || K % 64) return fail(RQ_ERR_INVALID_ARG, "bad shape rows=%d K=%d (K %% 64 == 0)", rows, K);
+  if (rows == 0) return ok();   // an empty tensor's pointer may be null
+  if (!codes || !block_scale || !out) return fail(RQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(codes) || !aligned16(block_scale) || !aligned16(out))
+    return fail(RQ_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+  rq::MxDequantLaunch a{codes, block_scale, out, rows, K, out_fp32 ? 1 : 0, num_sms()};
+  const cudaError_t e = rq::launch_mx_dequantize(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(RQ_ERR_CUDA, "dequantize launch failed: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+int64_t rq_mxfp4_layer_workspace(int32_t M, int32_t N, int32_t K) {
+  if (M < 0 || N <= 0 || K <= 0 || K % 64) return -1;
+  return up256((int64_t)M * (K / 2)) + up256(mx_tiles(M, K));
+}
+
+rq_status rq_mxfp4_layer(int32_t M, int32_t N, int32_t K, int32_t block, const uint16_t* X, const int32_t* rot,
+                         const uint8_t* w_codes, const uint8_t* w_bscale, void* workspace, int64_t workspace_bytes,
+                         void* Y, int32_t out_fp32, int32_t* status, void* stream) {
+  const int64_t need = rq_mxfp4_layer_workspace(M, N, K);
+  if (need < 0) return fail(RQ_ERR_INVALID_ARG, "bad shape M=%d N=%d K=%d (K %% 64 == 0)", M, N, K);
+  rq_status s = check_block(K, block);
+  if (s != RQ_OK) return s;
+  if (workspace_bytes < need)
+    return fail(RQ_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
+  if (M == 0) return ok();   // an empty tensor's pointer may be null
+  if (!workspace || !w_codes || !w_bscale || !Y) return fail(RQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(workspace) || !aligned16(w_codes) || !aligned16(w_bscale) || !aligned16(Y))
+    return fail(RQ_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  uint8_t* bscale = codes + up256((int64_t)M * (K / 2));
+  s = run_k1(RQ_MXFP4, false, X, M, K, block, rot, nullptr, nullptr, 0, nullptr, codes, nullptr, bscale,
+                             status, stream);
+  if (s != RQ_OK) return s;
+  return linear_impl(RQ_MXFP4, RQ_MXFP4, M, N, K, codes, nullptr, bscale, nullptr, w_codes, nullptr, w_bscale, nullptr,
+                     nullptr, nullptr, nullptr, nullptr, 0, Y, out_fp32, status, stream);
+}
+
+static rq_status moe_shape(int32_t T, int32_t K, int32_t I, int32_t E, int32_t top_k) {
+  if (T < 0 || K <= 0 || I <= 0 || E <= 0 || top_k <= 0)
+    return fail(RQ_ERR_INVALID_ARG, "bad shape T=%d K=%d I=%d E=%d top_k=%d", T, K, I, E, top_k);
+  if (T > RQ_MOE_MAX_TOKENS) return fail(RQ_ERR_UNSUPPORTED, "T=%d: at most %d tokens", T, RQ_MOE_MAX_TOKENS);
+  if (E > RQ_MOE_MAX_EXPERTS) return fail(RQ_ERR_UNSUPPORTED, "E=%d: at most %d experts", E, RQ_MOE_MAX_EXPERTS);
+  if (top_k > E || top_k > RQ_MOE_MAX_TOP_K)
+    return fail(RQ_ERR_INVALID_ARG, "top_k=%d: at most E=%d and %d", top_k, E, RQ_MOE_MAX_TOP_K);
+  if (K % 64 || K > 16384) return fail(RQ_ERR_INVALID_ARG, "K=%d must be a multiple of 64, at most 16384", K);
+  if (I % 128 || I > 16384) return fail(RQ_ERR_INVALID_ARG, "I=%d must be a multiple of 128, at most 16384", I);
+  return RQ_OK;
+}
+
+int64_t rq_mxfp4_moe_workspace(int32_t T, int32_t K, int32_t I, int32_t E, int32_t top_k) {
+  if (moe_shape(T, K, I, E, top_k) != RQ_OK) return -1;
+  return (int64_t)rq::moe_workspace_bytes(T, K, I, E, top_k);
+}
+
+rq_status rq_mxfp4_moe(int32_t T, int32_t K, int32_t I, int32_t E, int32_t top_k, int32_t renorm, const uint16_t* X,
+                       const uint16_t* router, int32_t block, const int32_t* rot, const uint8_t* w1_codes,
+                       const uint8_t* w1_bscale, int32_t block2, const uint8_t* w2_codes, const uint8_t* w2_bscale,
+                       int32_t* topk_idx, float* topk_weight, void* workspace, int64_t workspace_bytes, void* Y,
+                       int32_t out_fp32, int32_t* status, void* stream) {
+  rq_status s = moe_shape(T, K, I, E, top_k);
+  if (s == RQ_OK) s = check_block(K, block);
+  if (s != RQ_OK) return s;
+  if (block2 < 16 || block2 > 128 || !pow2(block2))
+    return fail(RQ_ERR_UNSUPPORTED, "block2 %d: a power of two from 16 to 128", block2);
+  const int64_t need = (int64_t)rq::moe_workspace_bytes(T, K, I, E, top_k);
+  if (workspace_bytes < need)
+    return fail(RQ_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
+  if (T == 0) return ok();   // an empty tensor's pointer may be null
+  const void* ptrs[] = {X, router, rot, w1_codes, w1_bscale, w2_codes, w2_bscale, topk_idx, topk_weight, workspace, Y};
+  for (const void* q : ptrs) {
+    if (!q) return fail(RQ_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(q)) return fail(RQ_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+  }
+  rq::MoeLaunch a{};
+  a.T = T; a.K = K; a.I = I; a.E = E; a.top_k = top_k; a.renorm = renorm ? 1 : 0;
+  a.block = block; a.block2 = block2; a.out_fp32 = out_fp32 ? 1 : 0;
+  a.x = X; a.router = router; a.rot = rot;
+  a.w1 = w1_codes; a.w1_sf = w1_bscale; a.w2 = w2_codes; a.w2_sf = w2_bscale;
+  a.idx = topk_idx; a.wts = topk_weight;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.Y = Y;
+  a.inv_sqrt_b = (float)(1.0 / std::sqrt((double)block));
+  a.inv_sqrt_b2 = (float)(1.0 / std::sqrt((double)block2));
+  a.status = status;
+  a.num_sms = num_sms();
+  a.wait_ns = g_wait_ns.load();
+  a.inject_tx = g_inject_tx.load();
+  const cudaError_t e = rq::launch_moe(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(RQ_ERR_CUDA, "expert layer launch failed: %s", cudaGetErrorString(e));
   return ok();
 }
 

@@ -10,6 +10,7 @@
 #define RQ_FMT_LM4 4
 #define RQ_FMT_INT4A 5
 #define RQ_FMT_INT8 6
+#define RQ_FMT_MXFP4 7
 
 namespace rq {
 
@@ -87,5 +88,34 @@ struct PcaLaunch {
 };
 
 cudaError_t launch_pca(const PcaLaunch& a, cudaStream_t st);
+
+// MXFP4 codes -> values
+struct MxDequantLaunch {
+  const uint8_t* codes;
+  const uint8_t* bscale;
+  void* out;
+  int rows, K, out_fp32, num_sms;
+};
+cudaError_t launch_mx_dequantize(const MxDequantLaunch& a, cudaStream_t st);
+
+// mixture-of-experts layer on MXFP4 experts (at most 64 tokens)
+struct MoeLaunch {
+  int T, K, I, E, top_k, renorm, block, block2, out_fp32;
+  const uint16_t* x;
+  const uint16_t* router;
+  const int32_t* rot;
+  const uint8_t *w1, *w1_sf, *w2, *w2_sf;
+  int32_t* idx;
+  float* wts;
+  uint8_t* ws;
+  void* Y;
+  float inv_sqrt_b, inv_sqrt_b2;
+  int32_t* status;
+  int num_sms;
+  uint64_t wait_ns;
+  uint32_t inject_tx;
+};
+size_t moe_workspace_bytes(int T, int K, int I, int E, int top_k);
+cudaError_t launch_moe(const MoeLaunch& a, cudaStream_t st);
 
 }  // namespace rq

@@ -36,6 +36,7 @@
 #include <cstring>
 
 #include "rq_internal.h"
+#include "rq_mx.cuh"
 #include "rq_ptx.cuh"
 
 namespace rq {
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(K1_THREADS, IPW == 1 ? 2 : 1) k1_rotate_quanti
           for (int m = 1; m < (L < 4 ? L : 4); m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, m));
           red[s] = amax;
           if constexpr (IPW == 1) publish(ri, bk, amax);
-        } else {
+        } else if constexpr (FMT != RQ_FMT_MXFP4) {   // MXFP4 has no row scale
 #pragma unroll
           for (int m = 1; m < L; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, m));
           red[s] = amax;
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(K1_THREADS, IPW == 1 ? 2 : 1) k1_rotate_quanti
         }
       }
     }
-    if constexpr (IPW > 1) {
+    if constexpr (IPW > 1 && FMT != RQ_FMT_MXFP4) {
 #pragma unroll
       for (int s = 0; s < IPW; ++s) {
         const int item = slot0 + s * SLOTS;
@@ -580,8 +581,9 @@ __global__ void __launch_bounds__(K1_THREADS, IPW == 1 ? 2 : 1) k1_rotate_quanti
         uint32_t pk[4] = {0u, 0u, 0u, 0u};   // 32 codes, nibble e at bits 4(e%8) of word e/8
         // row (or group) scale, derived by every lane from the block partials;
         // the first lane of the row's (group's) first block writes it out
-        float mlt;
-        if constexpr (FMT == RQ_FMT_INT4) {
+        float mlt = 0.f;
+        if constexpr (FMT == RQ_FMT_MXFP4) {
+        } else if constexpr (FMT == RQ_FMT_INT4) {
           const float amax = __uint_as_float(amax_bits[ri * ngrp + (WEIGHT ? i0 / 128 : 0)]);
           mlt = amax > 0.f ? __fdiv_rn(7.0f, amax) : 0.f;
           if (WEIGHT ? (i0 % 128 == 0) : (bk == 0 && lq == 0)) {
@@ -638,6 +640,16 @@ __global__ void __launch_bounds__(K1_THREADS, IPW == 1 ? 2 : 1) k1_rotate_quanti
               pk[e >> 4] |= c << (4 * (e & 7) + 2 * ((e >> 3) & 1));   // nibble e%8: elements e%8, e%8+8
             }
           }
+        } else if constexpr (FMT == RQ_FMT_MXFP4) {   // the lane's 32 coordinates are one block
+          float a32 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a32 = fmax_nan(a32, fabsf(v[e]));
+          const uint32_t sb = mx_scale_byte(a32);
+          const float inv = mx_inv_scale(sb);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            pk[e >> 3] |= (sb == 255u ? 0u : (uint32_t)cvt_e2m1x2(__fmul_rn(v[e + 1], inv), __fmul_rn(v[e], inv))) << (4 * (e & 7));
+          p.bscale[mx_sf_offset(row, i0 / 32, K)] = (uint8_t)sb;
         } else {  // NVFP4: two 16-element groups per lane
           const float inv_t = mlt;
           uint16_t sbs = 0;
@@ -824,6 +836,7 @@ cudaError_t launch_k1_fmt(const K1Launch& a, cudaStream_t st) {
     case RQ_FMT_LM16: return launch_k1_mode<L, RQ_FMT_LM16>(a, st);
     case RQ_FMT_LM4: return launch_k1_mode<L, RQ_FMT_LM4>(a, st);
     case RQ_FMT_NVFP4: return launch_k1_mode<L, RQ_FMT_NVFP4>(a, st);
+    case RQ_FMT_MXFP4: return launch_k1_mode<L, RQ_FMT_MXFP4>(a, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -41,6 +41,7 @@
 #include <cstring>
 
 #include "rq_internal.h"
+#include "rq_mx.cuh"
 #include "rq_ptx.cuh"
 
 namespace rq {
@@ -161,8 +162,9 @@ struct SqTree {
 
 template <int FMT, bool WEIGHT, int B, int SEG>
 __global__ void __launch_bounds__(R_THREADS, 1) k1r_kernel(const __grid_constant__ K1RParams p) {
-  static_assert(SEG == 128 || (B <= 64 && (FMT == RQ_FMT_LM16 || FMT == RQ_FMT_LM4 || FMT == RQ_FMT_NVFP4)),
-                "64-wide segments carry codebook and NVFP4 rows with blocks up to 64");
+  static_assert(SEG == 128 || (B <= 64 && (FMT == RQ_FMT_LM16 || FMT == RQ_FMT_LM4 || FMT == RQ_FMT_NVFP4 ||
+                                            FMT == RQ_FMT_MXFP4)),
+                "64-wide segments carry codebook, NVFP4 and MXFP4 rows with blocks up to 64");
   constexpr int TS = SEG + 4;
   constexpr int T = B > SEG ? B / SEG : 1;        // threads per Hadamard block (<= F)
   const int F = p.F;
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(R_THREADS, 1) k1r_kernel(const __grid_constant
         const float sc = amax > 0.f ? __fdiv_rn(amax, 7.0f) : 0.f;
         pt[rl * pstride + seg * NPART] = __fmul_rn(sc, (float)csum);
       }
-    } else {
+    } else if constexpr (FMT != RQ_FMT_MXFP4) {   // MXFP4 has no row scale
       float mx = 0.f, mn = 0.f;
       if constexpr (FMT == RQ_FMT_INT4A) {
         mx = v[0];
@@ -393,9 +395,10 @@ __global__ void __launch_bounds__(R_THREADS, 1) k1r_kernel(const __grid_constant
 
     // ------------------------------------------------------------ phase B
     if (!live) continue;
-    float mlt;
+    float mlt = 0.f;
     float zpt = 0.f;
-    if constexpr (FMT == RQ_FMT_LM16 || FMT == RQ_FMT_LM4) {
+    if constexpr (FMT == RQ_FMT_MXFP4) {
+    } else if constexpr (FMT == RQ_FMT_LM16 || FMT == RQ_FMT_LM4) {
       // the row's sum of squares: block partials added in block order
       const float* pr = pt + rl * pstride;
       float ss = pr[0];
@@ -516,6 +519,37 @@ __global__ void __launch_bounds__(R_THREADS, 1) k1r_kernel(const __grid_constant
 #pragma unroll
         for (int c = 0; c < SEG / 64; ++c) dst[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       }
+    } else if constexpr (FMT == RQ_FMT_MXFP4) {   // SEG / 32 blocks of 32 elements
+      uint32_t pk[SEG / 8];
+      uint32_t sbw = 0u;
+#pragma unroll
+      for (int bq = 0; bq < SEG / 32; ++bq) {
+        float* u = v + 32 * bq;
+        float a32 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) a32 = fmax_nan(a32, fabsf(u[e]));
+        const uint32_t sb = mx_scale_byte(a32);
+        const float inv = mx_inv_scale(sb);
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t w = 0u;
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            float a = u[e + k], b = u[e + k + 1];
+            mul2s(a, b, inv);
+            w |= (sb == 255u ? 0u : (uint32_t)cvt_e2m1x2(b, a)) << (4 * k);
+          }
+          pk[4 * bq + (e >> 3)] = w;
+        }
+        sbw |= sb << (8 * bq);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.codes + (size_t)row * (K / 2) + (size_t)seg * (SEG / 2));
+#pragma unroll
+      for (int c = 0; c < SEG / 32; ++c) dst[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+      // the segment's scale bytes are adjacent in the tile layout
+      uint8_t* sf = p.bscale + mx_sf_offset(row, seg * (SEG / 32), K);
+      if constexpr (SEG == 128) *reinterpret_cast<uint32_t*>(sf) = sbw;
+      else *reinterpret_cast<uint16_t*>(sf) = (uint16_t)sbw;
     } else {   // NVFP4: SEG / 16 groups of 16 elements
       uint32_t pk[SEG / 8];
       uint32_t sbw[2] = {0u, 0u};
@@ -674,9 +708,9 @@ cudaError_t launch_r(const K1Launch& a, cudaStream_t st) {
 bool k1r_supports(const K1Launch& a) {
   if (a.U) return false;
   if (a.K % 64) return false;
-  // 64-wide segments: codebook and NVFP4 codes with blocks up to 64, one rotation
+  // 64-wide segments: codebook, NVFP4 and MXFP4 codes with blocks up to 64, one rotation
   if (a.K % 128 && (a.block > 64 || a.rot2 || a.wz ||
-                    (a.fmt != RQ_FMT_LM16 && a.fmt != RQ_FMT_LM4 && a.fmt != RQ_FMT_NVFP4)))
+                    (a.fmt != RQ_FMT_LM16 && a.fmt != RQ_FMT_LM4 && a.fmt != RQ_FMT_NVFP4 && a.fmt != RQ_FMT_MXFP4)))
     return false;
   if (a.rot2 && a.K > 8192) return false;   // the FP32 row copy of the double rotation
   switch (a.block) {
@@ -694,6 +728,7 @@ cudaError_t launch_r_t64(const K1Launch& a, cudaStream_t st) {
       case RQ_FMT_LM16: return a.weight ? launch_r<RQ_FMT_LM16, true, BS, 64>(a, st) : launch_r<RQ_FMT_LM16, false, BS, 64>(a, st);
       case RQ_FMT_LM4: return a.weight ? launch_r<RQ_FMT_LM4, true, BS, 64>(a, st) : cudaErrorInvalidValue;
       case RQ_FMT_NVFP4: return a.weight ? launch_r<RQ_FMT_NVFP4, true, BS, 64>(a, st) : launch_r<RQ_FMT_NVFP4, false, BS, 64>(a, st);
+      case RQ_FMT_MXFP4: return launch_r<RQ_FMT_MXFP4, false, BS, 64>(a, st);
     }
   }
   return cudaErrorInvalidValue;
@@ -702,6 +737,7 @@ cudaError_t launch_r_t64(const K1Launch& a, cudaStream_t st) {
 template <int BS>
 cudaError_t launch_r_t(const K1Launch& a, cudaStream_t st) {
   if (a.K % 128) return launch_r_t64<BS>(a, st);
+  if (a.fmt == RQ_FMT_MXFP4) return launch_r<RQ_FMT_MXFP4, false, BS, 128>(a, st);   // the same for both sides
   if (a.weight) {
     switch (a.fmt) {
       case RQ_FMT_INT4: return launch_r<RQ_FMT_INT4, true, BS, 128>(a, st);

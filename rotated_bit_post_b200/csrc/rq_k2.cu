@@ -201,6 +201,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int n) {
 __host__ __device__ constexpr uint32_t idesc_nvf4(int n) {
   return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
 }
+// MXFP4: E8M0 scales (bit 23), one per 32 elements; a 64-wide instruction takes
+// bytes id, id + 1 of each scale word (id 0 or 2: bits 4-5 for B, 29-30 for A).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int n, uint32_t id) {
+  return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(BM >> 4) << 24) | (id << 29);
+}
 
 // ===================================================================== shared
 // Named barrier among the epilogue warps.
@@ -1155,10 +1161,12 @@ __global__ void __launch_bounds__(fp8_threads<BN, GROUPED>(), 1) gemm_fp8_kernel
 // Per stage: packed A 128 x 128 B, packed B BN x 128 B (256 E2M1 per row, 128B
 // swizzle), scale tiles 128 x 16 B and BN x 16 B (4 chunks of 32 x 16 B per
 // 128 rows, the layout tcgen05.cp 32x128b.warpx4 reads).
-template <int BN>
+// MXFP4 (MX): half the scale bytes, 128 x 8 B and BN x 8 B.
+template <int BN, bool MX>
 struct Nvf4Plan {
   static constexpr int S = BN == 256 ? 4 : 5;
-  static constexpr int PA = BM * 128, PB = BN * 128, SA = BM * 16, SB = BN * 16;
+  static constexpr int SCT = MX ? 2 : 4;   // 512-byte scale tiles per 128 rows and K step
+  static constexpr int PA = BM * 128, PB = BN * 128, SA = SCT * 512, SB = BN / 128 * SCT * 512;
   static constexpr int STAGE = PA + PB + SA + SB;
   static constexpr bool LR = BN == 128;   // the low-rank branch runs with BN = 128 only
   static constexpr int NACC = BN == 256 ? 1 : 2;
@@ -1182,9 +1190,10 @@ struct Nvf4Plan {
 // so the epilogue's length is a pipeline bubble).
 constexpr int NVF4_THREADS = 384;
 
-template <int BN>
+template <int BN, bool MX>
 __global__ void __launch_bounds__(NVF4_THREADS, 1) gemm_nvf4_kernel(const __grid_constant__ TMaps tm, const __grid_constant__ GemmParams p) {
-  using P = Nvf4Plan<BN>;
+  using P = Nvf4Plan<BN, MX>;
+  constexpr int SCT = P::SCT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -1209,7 +1218,8 @@ __global__ void __launch_bounds__(NVF4_THREADS, 1) gemm_nvf4_kernel(const __grid
   // 256-wide K steps; the last may hold 1-3 of its four 64-wide scale tiles
   // (K % 64 == 0): only those are copied and multiplied
   const int nk = (p.K + 255) / 256;
-  const int ktiles64 = p.K / 64;          // scale tiles per 128 rows
+  const int ktiles64 = p.K / 64;
+  const int sct = MX ? (p.K + 127) / 128 : ktiles64;   // scale tiles per 128 rows
   const bool lr = P::LR && p.has_lr;
   const int nN = (p.N + BN - 1) / BN, nM = (p.M + BM - 1) / BM;
   const int ntiles = nM * nN;
@@ -1250,22 +1260,22 @@ __global__ void __launch_bounds__(NVF4_THREADS, 1) gemm_nvf4_kernel(const __grid
       int lr_issued = 0;
       for (int tile = blockIdx.x; tile < ntiles && !*abort_flag; tile += gridDim.x, ++tc) {
         const int m0 = (tile / nN) * BM, n0 = (tile % nN) * BN;
-        const uint8_t* sfa_src = p.a_bscale + (size_t)(m0 / 128) * ktiles64 * 512;
+        const uint8_t* sfa_src = p.a_bscale + (size_t)(m0 / 128) * sct * 512;
         // weight scale tiles that exist (the last tile column may cover only 128 rows)
         const int nb_valid = min(BN / 128, (p.N + 127) / 128 - n0 / 128);
         for (int kt = 0; kt < nk; ++kt, ++kc) {
           const int s = kc % P::S;
           if (kc >= P::S && !mbar_wait(&empty[s], ((kc / P::S) - 1) & 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns)) break;
           uint8_t* st = smem + s * P::STAGE;
-          const uint32_t sfb = (uint32_t)min(4, ktiles64 - kt * 4) * 512;   // scale bytes per 128 rows
+          const uint32_t sfb = (uint32_t)min(SCT, sct - kt * SCT) * 512;   // scale bytes per 128 rows
           mbar_expect_tx(&full[s], P::PA + P::PB + sfb + nb_valid * sfb + (kc == 0 ? p.inject_tx : 0u));
           tma_load_2d(st, &tm.a, kt * 128, m0, &full[s]);
           tma_load_2d(st + P::PA, &tm.b, kt * 128, n0, &full[s]);
-          // up to 4 scale chunks (k tiles of 64) x 512 B, contiguous in the K1 layout
-          bulk_g2s(st + P::PA + P::PB, sfa_src + (size_t)kt * 4 * 512, sfb, &full[s]);
+          // up to SCT scale tiles x 512 B, contiguous in the K1 layout
+          bulk_g2s(st + P::PA + P::PB, sfa_src + (size_t)kt * SCT * 512, sfb, &full[s]);
           for (int nb = 0; nb < nb_valid; ++nb)
-            bulk_g2s(st + P::PA + P::PB + P::SA + nb * 2048,
-                     p.w_bscale + ((size_t)(n0 / 128 + nb) * ktiles64 + (size_t)kt * 4) * 512, sfb, &full[s]);
+            bulk_g2s(st + P::PA + P::PB + P::SA + nb * SCT * 512,
+                     p.w_bscale + ((size_t)(n0 / 128 + nb) * sct + (size_t)kt * SCT) * 512, sfb, &full[s]);
         }
         if (lr) {   // after the K tiles (see the codebook kernel)
           if (tc > 0 && !mbar_wait(lrsmem_empty, (tc - 1) & 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns)) break;
@@ -1306,9 +1316,15 @@ __global__ void __launch_bounds__(NVF4_THREADS, 1) gemm_nvf4_kernel(const __grid
           const int kkn = min(4, ktiles64 - kt * 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            if (kk < kkn)
-              umma_nvf4(tmem + ab * BN, smem_desc(st + kk * 32, 16, 1024, 2), smem_desc(st + P::PA + kk * 32, 16, 1024, 2),
-                      idesc, t_sfa + kk * 4, t_sfb + kk * (BN / 32), (kt > 0 || kk > 0) ? 1u : 0u);
+            if (kk < kkn) {
+              const uint64_t ad = smem_desc(st + kk * 32, 16, 1024, 2), bd = smem_desc(st + P::PA + kk * 32, 16, 1024, 2);
+              const uint32_t acc = (kt > 0 || kk > 0) ? 1u : 0u;
+              if constexpr (MX)   // two 64-wide halves share a scale tile
+                umma_mxf4(tmem + ab * BN, ad, bd, idesc_mxf4(BN, (kk & 1) * 2), t_sfa + (kk >> 1) * 4,
+                          t_sfb + (kk >> 1) * (BN / 32), acc);
+              else
+                umma_nvf4(tmem + ab * BN, ad, bd, idesc, t_sfa + kk * 4, t_sfb + kk * (BN / 32), acc);
+            }
           tc_commit(&empty[s]);
           tc_commit(&sfempty[sl]);
         }
@@ -1353,11 +1369,11 @@ __global__ void __launch_bounds__(NVF4_THREADS, 1) gemm_nvf4_kernel(const __grid
           const uint32_t sfa = sbase + s * P::STAGE + P::PA + P::PB, sfb = sfa + P::SA;
           const uint32_t t_a = tmem + 256 + sl * SF_COLS, t_b = t_a + 16;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
+          for (int kk = 0; kk < SCT; ++kk) {
             tc_cp_32x128b_warpx4(t_a + kk * 4, smem_desc(sfa + kk * 512, 16, 128, 0));
 #pragma unroll
             for (int nb = 0; nb < BN / 128; ++nb)
-              tc_cp_32x128b_warpx4(t_b + kk * (BN / 32) + nb * 4, smem_desc(sfb + nb * 2048 + kk * 512, 16, 128, 0));
+              tc_cp_32x128b_warpx4(t_b + kk * (BN / 32) + nb * 4, smem_desc(sfb + nb * SCT * 512 + kk * 512, 16, 128, 0));
           }
           tc_commit(&sffull[sl]);
         }
@@ -1379,10 +1395,14 @@ __global__ void __launch_bounds__(NVF4_THREADS, 1) gemm_nvf4_kernel(const __grid
     for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x, ++tc) {
       const int m0 = (tile / nN) * BM, n0 = (tile % nN) * BN;
       const int row = m0 + q * 32 + lane;
-      const float sa = row < p.M ? __ldg(p.a_scale + row) : 0.f;
+      const float sa = MX ? 1.f : row < p.M ? __ldg(p.a_scale + row) : 0.f;
       const uint32_t ab = tc % P::NACC;
       float* sw = sc_slots + (tc & 1) * BN;
-      load_scales_smem(sw, p.w_scale, n0, p.N, BN, tid, 256);
+      if constexpr (MX) {   // no row scales
+        for (int i = tid; i < BN; i += 256) sw[i] = 1.f;
+      } else {
+        load_scales_smem(sw, p.w_scale, n0, p.N, BN, tid, 256);
+      }
       epi_bar_n<256>();
       ok = ok && mbar_wait(&accfull[ab], (tc / P::NACC) & 1, p.status, ST_TIMEOUT_MMA, abort_flag, p.wait_ns) &&
            (!lr || mbar_wait(lrdone, tc & 1, p.status, ST_TIMEOUT_MMA, abort_flag, p.wait_ns));
@@ -1525,7 +1545,8 @@ cudaError_t launch_gemm(const GemmLaunch& a, cudaStream_t st, const char** why) 
   gp.a_zp = a.a_zp; gp.w_zsum = a.w_zsum;
   gp.tma_store = 0;
 
-  const bool nvf4 = a.a_fmt == RQ_FMT_NVFP4;
+  const bool mxf4 = a.a_fmt == RQ_FMT_MXFP4;
+  const bool nvf4 = a.a_fmt == RQ_FMT_NVFP4 || mxf4;
   const bool grouped = a.w_fmt == RQ_FMT_INT4;
   // 128 x 256 tiles unless the INT4 group epilogue or the low-rank branch needs the TMEM
   const int BN = (grouped || gp.has_lr) ? 128 : 256;
@@ -1545,8 +1566,12 @@ cudaError_t launch_gemm(const GemmLaunch& a, cudaStream_t st, const char** why) 
     ok &= make_map_2d(&tm.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, a.K / 2, a.N, a.K / 2, 128, BN,
                       CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) { *why = "cuTensorMapEncodeTiled failed"; return cudaErrorInvalidValue; }
-    if (BN == 256) return launch(gemm_nvf4_kernel<256>, Nvf4Plan<256>::BYTES, grid, NVF4_THREADS, tm, gp, st);
-    return launch(gemm_nvf4_kernel<128>, Nvf4Plan<128>::BYTES, grid, NVF4_THREADS, tm, gp, st);
+    if (mxf4) {
+      if (BN == 256) return launch(gemm_nvf4_kernel<256, true>, Nvf4Plan<256, true>::BYTES, grid, NVF4_THREADS, tm, gp, st);
+      return launch(gemm_nvf4_kernel<128, true>, Nvf4Plan<128, true>::BYTES, grid, NVF4_THREADS, tm, gp, st);
+    }
+    if (BN == 256) return launch(gemm_nvf4_kernel<256, false>, Nvf4Plan<256, false>::BYTES, grid, NVF4_THREADS, tm, gp, st);
+    return launch(gemm_nvf4_kernel<128, false>, Nvf4Plan<128, false>::BYTES, grid, NVF4_THREADS, tm, gp, st);
   }
   const bool w2 = a.w_fmt == RQ_FMT_LM4;
   if (!a.out_fp32 && a.N % 8 == 0) {   // (the map's row pitch must be a multiple of 16 bytes)

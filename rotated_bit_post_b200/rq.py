@@ -13,16 +13,16 @@ import os
 
 import numpy as np
 
-INT4, LM16, NVFP4, LM4, INT4A, INT8 = 1, 2, 3, 4, 5, 6
+INT4, LM16, NVFP4, LM4, INT4A, INT8, MXFP4 = 1, 2, 3, 4, 5, 6, 7
 NOALLOC_MAX_ELEMS = 4194304   # RQ_NOALLOC_MAX_ELEMS: the built-in workspace of the no-allocation call
-FORMATS = {"int4": INT4, "lm16": LM16, "nvfp4": NVFP4, "lm4": LM4, "int4a": INT4A, "int8": INT8}
+FORMATS = {"int4": INT4, "lm16": LM16, "nvfp4": NVFP4, "lm4": LM4, "int4a": INT4A, "int8": INT8, "mxfp4": MXFP4}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librq.so")
 
 _lib = None
 
-_c_i32, _c_u64, _c_p = ctypes.c_int32, ctypes.c_uint64, ctypes.c_void_p
+_c_i32, _c_i64, _c_u64, _c_p = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
 
 # (name, restype, argtypes) -- mirrors include/rq.h
 SIGNATURES = [
@@ -45,6 +45,14 @@ SIGNATURES = [
     ("rq_pca_rotate_quantize_act", _c_i32, [_c_p, _c_i32, _c_i32, _c_p, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
     ("rq_pca_quantize_weights", _c_i32, [_c_p, _c_i32, _c_i32, _c_p, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
     ("rq_pca_rotate_quantize_act_noalloc", _c_i32, [_c_p, _c_i32, _c_i32, _c_p, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    ("rq_mxfp4_dequantize", _c_i32, [_c_i32, _c_i32, _c_p, _c_p, _c_p, _c_i32, _c_p]),
+    ("rq_mxfp4_layer_workspace", _c_i64, [_c_i32, _c_i32, _c_i32]),
+    ("rq_mxfp4_layer", _c_i32,
+     [_c_i32, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p]),
+    ("rq_mxfp4_moe_workspace", _c_i64, [_c_i32] * 5),
+    ("rq_mxfp4_moe", _c_i32,
+     [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_i32, _c_p, _c_p, _c_p, _c_i32, _c_p, _c_p, _c_p,
+      _c_p, _c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p]),
     ("rq_read_status", _c_i32, [_c_p, _c_p, _c_p]),
     ("rq_last_error", ctypes.c_char_p, []),
     # include/rq_check.h
@@ -222,6 +230,66 @@ def rq_w4a4_linear2(M, N, K, a_codes, a_scale, a_zero_point, w_codes, w_scale, w
         _dev(Y), int(out_fp32), _dev(status), _stream(stream)))
 
 
+def _shape(what, t, elem_bytes, n):
+    """The buffer holds at least n elements of that many bytes."""
+    if t.element_size() != elem_bytes or t.numel() < n:
+        raise ValueError(f"{what}: {n} elements of {elem_bytes} bytes expected, "
+                         f"got {t.numel()} of {t.element_size()}")
+
+
+def rq_mxfp4_dequantize(codes, block_scale, out, out_fp32, stream=None):
+    """Values of MXFP4 codes [rows, K/2] -> out [rows, K], FP32 or BF16."""
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    _shape("block_scale", block_scale, 1, mx_sf_bytes(rows, K))
+    _shape("out", out, 4 if out_fp32 else 2, rows * K)
+    _check("rq_mxfp4_dequantize", lib().rq_mxfp4_dequantize(
+        rows, K, _dev(codes), _dev(block_scale), _dev(out), int(out_fp32), _stream(stream)))
+
+
+def rq_mxfp4_layer_workspace(M: int, N: int, K: int) -> int:
+    """Bytes of rq_mxfp4_layer's workspace (-1: a shape outside the limits)."""
+    return lib().rq_mxfp4_layer_workspace(M, N, K)
+
+
+def rq_mxfp4_layer(X, block, rot, w_codes, w_bscale, workspace, Y, out_fp32, status, stream=None):
+    """Y = Q(R X) W^T from BF16 rows, MXFP4 on both sides."""
+    M, K = X.shape
+    N = w_codes.shape[0]
+    _shape("rot", rot, 4, K)
+    _shape("w_codes", w_codes, 1, N * (K // 2))
+    _shape("w_bscale", w_bscale, 1, mx_sf_bytes(N, K))
+    _shape("Y", Y, 4 if out_fp32 else 2, M * N)
+    _check("rq_mxfp4_layer", lib().rq_mxfp4_layer(
+        M, N, K, block, _dev(X), _dev(rot), _dev(w_codes), _dev(w_bscale), _dev(workspace),
+        workspace.numel() * workspace.element_size(), _dev(Y), int(out_fp32), _dev(status), _stream(stream)))
+
+
+def rq_mxfp4_moe_workspace(T: int, K: int, I: int, E: int, top_k: int) -> int:
+    """Bytes of rq_mxfp4_moe's workspace (-1: a shape outside the limits)."""
+    return lib().rq_mxfp4_moe_workspace(T, K, I, E, top_k)
+
+
+def rq_mxfp4_moe(X, router, top_k, renorm, block, rot, w1_codes, w1_bscale, block2, w2_codes, w2_bscale, topk_idx,
+                 topk_weight, workspace, Y, out_fp32, status, stream=None):
+    """Mixture-of-experts layer: w1_codes [E, 2I, K/2] (gate rows, then up
+    rows), w2_codes [E, K, I/2]; routing out to topk_idx / topk_weight."""
+    T, K = X.shape
+    E, I = w1_codes.shape[0], w1_codes.shape[1] // 2
+    _shape("router", router, 2, E * K)
+    _shape("rot", rot, 4, K)
+    _shape("w1_codes", w1_codes, 1, E * 2 * I * (K // 2))
+    _shape("w1_bscale", w1_bscale, 1, E * mx_sf_bytes(2 * I, K))
+    _shape("w2_codes", w2_codes, 1, E * K * (I // 2))
+    _shape("w2_bscale", w2_bscale, 1, E * mx_sf_bytes(K, I))
+    _shape("topk_idx", topk_idx, 4, T * top_k)
+    _shape("topk_weight", topk_weight, 4, T * top_k)
+    _shape("Y", Y, 4 if out_fp32 else 2, T * K)
+    _check("rq_mxfp4_moe", lib().rq_mxfp4_moe(
+        T, K, I, E, top_k, int(renorm), _dev(X), _dev(router), block, _dev(rot), _dev(w1_codes), _dev(w1_bscale),
+        block2, _dev(w2_codes), _dev(w2_bscale), _dev(topk_idx), _dev(topk_weight), _dev(workspace),
+        workspace.numel() * workspace.element_size(), _dev(Y), int(out_fp32), _dev(status), _stream(stream)))
+
+
 def rq_read_status(status, stream=None):
     code = ctypes.c_int32(0)
     rc = lib().rq_read_status(_dev(status), _stream(stream), ctypes.byref(code))
@@ -260,13 +328,24 @@ def sf_bytes(rows: int, K: int) -> int:
     return ((rows + 127) // 128) * (K // 64) * 512
 
 
+def mx_sf_bytes(rows: int, K: int) -> int:
+    """Size of an MXFP4 block-scale buffer (128-row x 128-column tiles of 512 B)."""
+    return ((rows + 127) // 128) * ((K + 127) // 128) * 512
+
+
+def _block_scale(fmt, rows, K, device):
+    import torch
+    n = sf_bytes(rows, K) if fmt == NVFP4 else mx_sf_bytes(rows, K) if fmt == MXFP4 else 0
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
 def act_buffers(fmt: int, M: int, K: int, r: int = 0, device="cuda"):
     """Caller-owned output buffers for rq_rotate_quantize_act (torch, uninitialised)."""
     import torch
     out = {
         "codes": torch.empty((M, K // 2), dtype=torch.uint8, device=device),
         "scale": torch.empty(M, dtype=torch.float32, device=device),
-        "block_scale": torch.zeros(sf_bytes(M, K), dtype=torch.uint8, device=device) if fmt == NVFP4 else None,
+        "block_scale": _block_scale(fmt, M, K, device),
         "c": torch.empty((M, r), dtype=torch.int16, device=device) if r else None,
     }
     return out
@@ -278,6 +357,6 @@ def weight_buffers(fmt: int, N: int, K: int, r: int = 0, device="cuda"):
     return {
         "codes": torch.empty((N, cols), dtype=torch.uint8, device=device),
         "scale": torch.empty((K // 128, N) if fmt == INT4 else (N,), dtype=torch.float32, device=device),
-        "block_scale": torch.zeros(sf_bytes(N, K), dtype=torch.uint8, device=device) if fmt == NVFP4 else None,
+        "block_scale": _block_scale(fmt, N, K, device),
         "L": torch.empty((N, r), dtype=torch.int16, device=device) if r else None,
     }
