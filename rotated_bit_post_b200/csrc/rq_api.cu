@@ -300,7 +300,8 @@ static rq_status linear_impl(int32_t a_fmt, int32_t w_fmt, int32_t M, int32_t N,
                              const float* a_scale, const uint8_t* a_bscale, const float* a_zp, const uint8_t* w_codes,
                              const float* w_scale, const uint8_t* w_bscale, const float* w_zsum,
                              const uint8_t* a_lut, const uint8_t* w_lut, const uint16_t* c, const uint16_t* L,
-                             int32_t r, void* Y, int32_t out_fp32, int32_t* status, void* stream);
+                             int32_t r, void* Y, int32_t out_fp32, int32_t* status, void* stream,
+                             bool early_weights = false);
 
 rq_status rq_w4a4_linear(int32_t a_fmt, int32_t w_fmt, int32_t M, int32_t N, int32_t K, const uint8_t* a_codes,
                          const float* a_scale, const uint8_t* a_bscale, const uint8_t* w_codes,
@@ -325,7 +326,8 @@ static rq_status linear_impl(int32_t a_fmt, int32_t w_fmt, int32_t M, int32_t N,
                              const float* a_scale, const uint8_t* a_bscale, const float* a_zp, const uint8_t* w_codes,
                              const float* w_scale, const uint8_t* w_bscale, const float* w_zsum,
                              const uint8_t* a_lut, const uint8_t* w_lut, const uint16_t* c, const uint16_t* L,
-                             int32_t r, void* Y, int32_t out_fp32, int32_t* status, void* stream) {
+                             int32_t r, void* Y, int32_t out_fp32, int32_t* status, void* stream,
+                             bool early_weights) {
   const bool pair_ok = (a_fmt == RQ_INT4 && w_fmt == RQ_INT4) || (a_fmt == RQ_INT4A && w_fmt == RQ_INT4) ||
                        (a_fmt == RQ_INT8 && w_fmt == RQ_INT4) || (a_fmt == RQ_INT8 && w_fmt == RQ_INT8) ||
                        (a_fmt == RQ_LM16 && w_fmt == RQ_LM16) ||
@@ -392,6 +394,7 @@ static rq_status linear_impl(int32_t a_fmt, int32_t w_fmt, int32_t M, int32_t N,
   g.r = c ? r : 0;
   g.Y = Y;
   g.out_fp32 = out_fp32 ? 1 : 0;
+  g.early_weights = early_weights ? 1 : 0;
   g.status = status;
   g.num_sms = num_sms();
   g.wait_ns = g_wait_ns.load();
@@ -453,7 +456,7 @@ rq_status rq_mxfp4_layer(int32_t M, int32_t N, int32_t K, int32_t block, const u
                              status, stream);
   if (s != RQ_OK) return s;
   return linear_impl(RQ_MXFP4, RQ_MXFP4, M, N, K, codes, nullptr, bscale, nullptr, w_codes, nullptr, w_bscale, nullptr,
-                     nullptr, nullptr, nullptr, nullptr, 0, Y, out_fp32, status, stream);
+                     nullptr, nullptr, nullptr, nullptr, 0, Y, out_fp32, status, stream, true);
 }
 
 static rq_status moe_shape(int32_t T, int32_t K, int32_t I, int32_t E, int32_t top_k) {

@@ -61,6 +61,8 @@ struct GemmLaunch {
   int r;
   void* Y;
   int out_fp32;
+  int early_weights;       // MXFP4, few tokens: the kernel before this one on the stream does not write the
+                           // weights and started after everything before it had finished
   int32_t* status;
   int num_sms;
   uint64_t wait_ns;
@@ -115,6 +117,13 @@ struct MoeLaunch {
   uint64_t wait_ns;
   uint32_t inject_tx;
 };
+// MXFP4 products of at most MX_FEW_TOKENS tokens (rq_mxfew.cu)
+constexpr int MX_FEW_TOKENS = 64;
+cudaError_t launch_mx_few(const GemmLaunch& a, cudaStream_t st, const char** why);
+// gate/up and down products of an expert layer whose routing and activation
+// codes are in place; `active`: the most experts that T tokens can choose
+cudaError_t launch_moe_products(const MoeLaunch& a, const uint8_t* xq, const uint8_t* xq_sf, uint8_t* hq, uint8_t* hq_sf,
+                                int active, cudaStream_t st);
 size_t moe_workspace_bytes(int T, int K, int I, int E, int top_k);
 cudaError_t launch_moe(const MoeLaunch& a, cudaStream_t st);
 

@@ -5,11 +5,19 @@
 // The routing weight goes onto the hidden row before its quantization, so the
 // sum over a token's experts is one long contraction.
 //
-// Three launches: routing with the activation transform, gate/up products
-// with the hidden rows' quantization, down products with the sum.
+// Three launches, each a programmatic dependent of the one before: routing
+// with the activation transform (here), the gate/up products with the hidden
+// rows' quantization, the down products with the sum (rq_mxfew.cu).
+//
+// Routing: a cluster of eight CTAs per token.  Every CTA stages the token's
+// row, takes an eighth of the experts' logits (a warp per expert, 16-byte
+// reads; FP32 sums) and an eighth of the rotated blocks; the logits meet in the
+// first CTA's shared memory, where one warp picks the experts.  The split
+// keeps one token's pass over the router (E K 2 bytes) off a single SM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "rq_internal.h"
@@ -20,202 +28,169 @@ namespace rq {
 
 namespace {
 
-constexpr int MOE_TMAX = 64;    // tokens
-constexpr int MOE_EMAX = 256;   // experts
 constexpr int PREP_THREADS = 256;
+constexpr int PREP_CLUSTER = 8;
+constexpr int MOE_EMAX = 256;
 
-struct MoeParams {
+struct PrepParams {
   const uint16_t* x;
   const uint16_t* router;
   const int32_t* rot;
-  const uint8_t *w1, *w1_sf, *w2, *w2_sf;
   int32_t* idx;
   float* wts;
   uint8_t *xq, *xq_sf;   // T x K/2 codes, one row tile of scales
-  uint8_t *hq, *hq_sf;   // [active][T][I/2] codes, [active] row tiles of scales
-  void* Y;
-  int T, K, I, E, top_k, renorm, block, block2, out_fp32;
-  float inv_sqrt_b, inv_sqrt_b2;
-  int32_t* status;
+  int T, K, E, top_k, renorm, block;
+  float inv_sqrt_b;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// One warp transforms and quantizes 32 EPL rotated coordinates of row m from
+// `base`, EPL consecutive ones per lane, from the row staged in shared memory:
+// butterflies in ascending stride, inside the lane and then across lanes.
+template <int EPL>
+__device__ __forceinline__ void rotate_unit(const uint16_t* xs, const int32_t* rot, int base, int block, float isb, int m,
+                                            int K, uint8_t* codes, uint8_t* sf) {
+  const int lane = threadIdx.x & 31, k0 = base + lane * EPL;
+  float v[EPL];
 #pragma unroll
-  for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-  return v;
-}
-
-// ascending list of the experts that some token chose: bits[8] and their count
-__device__ __forceinline__ int active_bits(const int32_t* idx, int n, uint32_t* bits) {
-  if (threadIdx.x < 8) bits[threadIdx.x] = 0u;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const uint32_t e = (uint32_t)__ldcg(idx + i);
-    atomicOr(&bits[e >> 5], 1u << (e & 31));
+  for (int i = 0; i < EPL; ++i) {
+    const int32_t r = __ldg(rot + k0 + i);
+    v[i] = __uint_as_float(((uint32_t)xs[r & 0x7fffffff] << 16) ^ ((uint32_t)r & 0x80000000u));
   }
-  __syncthreads();
-  int c = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c += __popc(bits[i]);
-  return c;
-}
-// the a-th expert of the list (a < count)
-__device__ __forceinline__ int nth_active(const uint32_t* bits, int a) {
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    const int c = __popc(bits[i]);
-    if (a < c) return i * 32 + (int)__fns(bits[i], 0, a + 1);
-    a -= c;
-  }
-  return 0;
-}
-
-// Butterflies over `n` shared values in blocks of `b`, ascending strides, by the
-// whole CTA; ends with a barrier.
-__device__ void fwht_shared(float* v, int n, int b) {
-  for (int h = 1; h < b; h <<= 1) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < n / 2; i += blockDim.x) {
-      const int lo = (i / h) * 2 * h + i % h;
-      const float a = v[lo], c = v[lo + h];
-      v[lo] = __fadd_rn(a, c);
-      v[lo + h] = __fsub_rn(a, c);
-    }
-  }
-  __syncthreads();
-}
-
-// One warp quantizes 32 values (one block): lane l holds value l.
-__device__ __forceinline__ void quantize_warp(float y, int m, int kb, int K, uint8_t* codes, uint8_t* sf) {
-  const int lane = threadIdx.x & 31;
-  float a = fabsf(y);
+  for (int h = 1; h < EPL; h <<= 1) {   // EPL <= block unless it is 1
 #pragma unroll
-  for (int s = 16; s; s >>= 1) a = fmax_nan(a, __shfl_xor_sync(0xffffffffu, a, s));
-  const uint32_t sb = mx_scale_byte(a);
-  const float v = __fmul_rn(y, mx_inv_scale(sb));
-  const float hi = __shfl_down_sync(0xffffffffu, v, 1);
-  if (!(lane & 1)) codes[(size_t)m * (K / 2) + kb * 16 + lane / 2] = sb == 255u ? 0 : cvt_e2m1x2(hi, v);
-  if (lane == 0) sf[mx_sf_offset(m, kb, K)] = (uint8_t)sb;
-}
-
-// One CTA per token: logits, routing, rotation, quantization.
-__global__ void __launch_bounds__(PREP_THREADS) moe_prep_kernel(const MoeParams p) {
-  extern __shared__ float sm[];
-  float* v = sm;                 // K rotated values
-  __shared__ float logit[MOE_EMAX];
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint16_t* x = p.x + (size_t)t * p.K;
-  for (int i = threadIdx.x; i < p.K; i += blockDim.x) {
-    const int32_t r = p.rot[i];
-    const float a = bf16_bits_to_f32(x[r & 0x7fffffff]);
-    v[i] = r < 0 ? -a : a;
-  }
-  for (int e = warp; e < p.E; e += PREP_THREADS / 32) {
-    const uint16_t* w = p.router + (size_t)e * p.K;
-    float s = 0.f;
-    for (int i = lane; i < p.K; i += 32) s += bf16_bits_to_f32(w[i]) * bf16_bits_to_f32(x[i]);
-    s = warp_sum(s);
-    if (lane == 0) logit[e] = s;
-  }
-  fwht_shared(v, p.K, p.block);
-  for (int kb = warp; kb < p.K / 32; kb += PREP_THREADS / 32)
-    quantize_warp(__fmul_rn(v[kb * 32 + lane], p.inv_sqrt_b), t, kb, p.K, p.xq, p.xq_sf);
-  if (threadIdx.x == 0) {
-    float mx = -INFINITY, all = 0.f, sel = 0.f;
-    for (int e = 0; e < p.E; ++e) mx = fmaxf(mx, logit[e]);
-    for (int e = 0; e < p.E; ++e) all += expf(logit[e] - mx);
-    for (int j = 0; j < p.top_k; ++j) {
-      int best = -1;
-      for (int e = 0; e < p.E; ++e) {   // NaN logits rank as -inf; an expert is chosen once
-        bool used = false;
-        for (int q = 0; q < j; ++q) used |= p.idx[t * p.top_k + q] == e;
-        const float l = logit[e] == logit[e] ? logit[e] : -INFINITY;
-        const float b = best >= 0 ? (logit[best] == logit[best] ? logit[best] : -INFINITY) : 0.f;
-        if (!used && (best < 0 || l > b)) best = e;
+    for (int i = 0; i < EPL; ++i)
+      if (!(i & h)) {
+        const float a = v[i], b = v[i + h];
+        v[i] = __fadd_rn(a, b);
+        v[i + h] = __fsub_rn(a, b);
       }
-      p.idx[t * p.top_k + j] = best;
-      sel += expf(logit[best] - mx);
-    }
-    for (int j = 0; j < p.top_k; ++j)
-      p.wts[t * p.top_k + j] = __fdiv_rn(expf(logit[p.idx[t * p.top_k + j]] - mx), p.renorm ? sel : all);
   }
+  for (int s = 1; s * EPL < block; s <<= 1) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float o = __shfl_xor_sync(0xffffffffu, v[i], s);
+      v[i] = lane & s ? __fsub_rn(o, v[i]) : __fadd_rn(v[i], o);
+    }
+  }
+  float am = 0.f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    v[i] = __fmul_rn(v[i], isb);
+    am = fmax_nan(am, fabsf(v[i]));
+  }
+#pragma unroll
+  for (int s = 1; s < 32 / EPL; s <<= 1) am = fmax_nan(am, __shfl_xor_sync(0xffffffffu, am, s));
+  const uint32_t sb = mx_scale_byte(am);
+  const float inv = mx_inv_scale(sb);
+  uint8_t* dst = codes + (size_t)m * (K / 2) + k0 / 2;
+  if constexpr (EPL == 1) {
+    const float y = __fmul_rn(v[0], inv), up = __shfl_down_sync(0xffffffffu, y, 1);
+    if (!(lane & 1)) *dst = sb == 255u ? (uint8_t)0 : cvt_e2m1x2(up, y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; i += 2)
+      dst[i / 2] = sb == 255u ? (uint8_t)0 : cvt_e2m1x2(__fmul_rn(v[i + 1], inv), __fmul_rn(v[i], inv));
+  }
+  if (k0 % 32 == 0) sf[mx_sf_offset(m, k0 / 32, K)] = (uint8_t)sb;
 }
 
-// sum over a row's blocks of scale_w scale_x sum q_w q_x
-__device__ float mx_dot(const uint8_t* a, const uint8_t* a_sf, int am, const uint8_t* b, const uint8_t* b_sf, int bm, int K) {
-  float s = 0.f;
-  for (int kb = 0; kb < K / 32; ++kb) {
-    const uint4 qa = *reinterpret_cast<const uint4*>(a + (size_t)am * (K / 2) + kb * 16);
-    const uint4 qb = *reinterpret_cast<const uint4*>(b + (size_t)bm * (K / 2) + kb * 16);
-    const uint32_t wa[4] = {qa.x, qa.y, qa.z, qa.w}, wb[4] = {qb.x, qb.y, qb.z, qb.w};
-    float d = 0.f;
-    for (int i = 0; i < 4; ++i)
-      for (int e = 0; e < 8; ++e) d += e2m1_value(wa[i] >> (4 * e) & 15u) * e2m1_value(wb[i] >> (4 * e) & 15u);
-    s += d * mx_scale(a_sf[mx_sf_offset(am, kb, K)]) * mx_scale(b_sf[mx_sf_offset(bm, kb, K)]);
-  }
-  return s;
+// A logit as an unsigned key of the same order: -0 as +0, NaN as -infinity,
+// never 0 (the key of an expert that is taken or does not exist).
+__device__ __forceinline__ uint32_t logit_key(float l) {
+  if (l != l) l = -INFINITY;
+  const uint32_t b = __float_as_uint(l + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// CTA (active expert, 128 hidden channels): gate and up rows, hidden row, quantization.
-__global__ void __launch_bounds__(256) moe_gate_up_kernel(const MoeParams p) {
-  __shared__ uint32_t bits[8];
-  __shared__ float gu[256];
-  __shared__ float wt;
-  __shared__ int routed;
-  const int n = active_bits(p.idx, p.T * p.top_k, bits);
-  const int a = blockIdx.x, c0 = blockIdx.y * 128;
-  if (a >= n) return;
-  const int e = nth_active(bits, a);
-  const uint8_t* w1 = p.w1 + (size_t)e * 2 * p.I * (p.K / 2);
-  const uint8_t* s1 = p.w1_sf + (size_t)e * mx_sf_bytes(2 * p.I, p.K);
-  uint8_t* hq = p.hq + (size_t)a * p.T * (p.I / 2);
-  uint8_t* hs = p.hq_sf + (size_t)a * mx_sf_bytes(p.T, p.I);
-  const int c = threadIdx.x & 127;
-  const int row = (threadIdx.x < 128 ? 0 : p.I) + c0 + c;
-  for (int t = 0; t < p.T; ++t) {
-    if (threadIdx.x == 0) {
-      routed = 0;
-      for (int j = 0; j < p.top_k; ++j)
-        if (p.idx[t * p.top_k + j] == e) {
-          wt = p.wts[t * p.top_k + j];
-          routed = 1;
-        }
+__global__ void __launch_bounds__(PREP_THREADS) __cluster_dims__(PREP_CLUSTER, 1, 1)
+    moe_route_kernel(const __grid_constant__ PrepParams p) {
+  extern __shared__ __align__(16) uint16_t xs[];   // the token's row
+  __shared__ float logit[MOE_EMAX];
+  const int rank = (int)cluster_ctarank(), t = blockIdx.x / PREP_CLUSTER;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the gate/up kernel may be scheduled: it waits for this grid before it reads
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int chunks = p.K / 8;   // 16-byte units of a row
+  const uint4* xrow = reinterpret_cast<const uint4*>(p.x + (size_t)t * p.K);
+  for (int i = threadIdx.x; i < chunks; i += PREP_THREADS) reinterpret_cast<uint4*>(xs)[i] = __ldg(xrow + i);
+  __syncthreads();
+  // the first CTA's shared memory is written below: all CTAs have started
+  cluster_sync();
+  uint32_t home;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(home) : "r"(smem_u32(logit)), "r"(0));
+  for (int e = rank + warp * PREP_CLUSTER; e < p.E; e += PREP_CLUSTER * (PREP_THREADS / 32)) {
+    const uint4* w = reinterpret_cast<const uint4*>(p.router + (size_t)e * p.K);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll 8
+    for (int i = lane; i < chunks; i += 32) {
+      const uint4 a = __ldg(w + i), b = reinterpret_cast<const uint4*>(xs)[i];
+      s0 = fmaf(bf_lo(a.x), bf_lo(b.x), s0); s1 = fmaf(bf_hi(a.x), bf_hi(b.x), s1);
+      s0 = fmaf(bf_lo(a.y), bf_lo(b.y), s0); s1 = fmaf(bf_hi(a.y), bf_hi(b.y), s1);
+      s0 = fmaf(bf_lo(a.z), bf_lo(b.z), s0); s1 = fmaf(bf_hi(a.z), bf_hi(b.z), s1);
+      s0 = fmaf(bf_lo(a.w), bf_lo(b.w), s0); s1 = fmaf(bf_hi(a.w), bf_hi(b.w), s1);
     }
-    __syncthreads();
-    const float w = wt;
-    const bool on = routed != 0;
-    if (on) gu[threadIdx.x] = mx_dot(w1, s1, row, p.xq, p.xq_sf, t, p.K);
-    __syncthreads();
-    if (on && threadIdx.x < 128) {
-      const float g = gu[c], u = gu[c + 128];
-      gu[c] = __fmul_rn(w, __fmul_rn(__fdiv_rn(g, __fadd_rn(1.f, expf(-g))), u));
-    } else if (threadIdx.x < 128) {
-      gu[c] = 0.f;
+    s0 += s1;
+#pragma unroll
+    for (int m = 16; m; m >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, m);
+    if (lane == 0) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(home + e * 4), "f"(s0) : "memory");
+  }
+  // rotated blocks, `unit` coordinates (whole Hadamard blocks) per warp and turn
+  const int unit = p.block < 32 ? 32 : p.block;
+  for (int u = rank + warp * PREP_CLUSTER; u < p.K / unit; u += PREP_CLUSTER * (PREP_THREADS / 32)) {
+    switch (unit) {
+      case 32: rotate_unit<1>(xs, p.rot, u * 32, p.block, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
+      case 64: rotate_unit<2>(xs, p.rot, u * 64, 64, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
+      case 128: rotate_unit<4>(xs, p.rot, u * 128, 128, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
+      case 256: rotate_unit<8>(xs, p.rot, u * 256, 256, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
+      case 512: rotate_unit<16>(xs, p.rot, u * 512, 512, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
+      default: rotate_unit<32>(xs, p.rot, u * 1024, 1024, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
     }
-    fwht_shared(gu, 128, p.block2);
-    if (threadIdx.x < 128)
-      quantize_warp(__fmul_rn(gu[c], p.inv_sqrt_b2), t, (c0 + c) / 32, p.I, hq, hs);
-    __syncthreads();
   }
-}
-
-// CTA (128 output channels, token): the sum over the active experts, in order.
-__global__ void __launch_bounds__(128) moe_down_kernel(const MoeParams p) {
-  __shared__ uint32_t bits[8];
-  const int n = active_bits(p.idx, p.T * p.top_k, bits);
-  const int row = blockIdx.x * 128 + threadIdx.x, t = blockIdx.y;
-  if (row >= p.K) return;
-  float s = 0.f;
-  for (int a = 0; a < n; ++a) {
-    const int e = nth_active(bits, a);
-    bool on = false;
-    for (int j = 0; j < p.top_k; ++j) on |= p.idx[t * p.top_k + j] == e;
-    if (on)
-      s += mx_dot(p.w2 + (size_t)e * p.K * (p.I / 2), p.w2_sf + (size_t)e * mx_sf_bytes(p.K, p.I), row,
-                  p.hq + (size_t)a * p.T * (p.I / 2), p.hq_sf + (size_t)a * mx_sf_bytes(p.T, p.I), t, p.I);
+  cluster_sync();
+  if (rank != 0 || warp != 0) return;
+  // ------------------------------------------------------------ the top_k experts
+  float l[MOE_EMAX / 32];
+  uint32_t key[MOE_EMAX / 32];
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < MOE_EMAX / 32; ++i) {
+    const int e = i * 32 + lane;
+    l[i] = e < p.E ? logit[e] : -INFINITY;
+    key[i] = e < p.E ? logit_key(l[i]) : 0u;
+    mx = fmaxf(mx, l[i]);   // (a NaN is left out)
   }
-  if (p.out_fp32) static_cast<float*>(p.Y)[(size_t)t * p.K + row] = s;
-  else static_cast<__nv_bfloat16*>(p.Y)[(size_t)t * p.K + row] = __float2bfloat16_rn(s);
+#pragma unroll
+  for (int m = 16; m; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+  float all = 0.f;
+#pragma unroll
+  for (int i = 0; i < MOE_EMAX / 32; ++i)
+    if (i * 32 + lane < p.E) all += expf(l[i] - mx);
+#pragma unroll
+  for (int m = 16; m; m >>= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
+  float sel = 0.f, mine = 0.f;
+  int chosen = 0;
+  for (int j = 0; j < p.top_k; ++j) {
+    uint32_t k = 0u, e = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < MOE_EMAX / 32; ++i)
+      if (key[i] > k) { k = key[i]; e = i * 32 + lane; }   // the lowest of this lane's equals
+    const uint32_t top = __reduce_max_sync(0xffffffffu, k);
+    const uint32_t best = __reduce_min_sync(0xffffffffu, k == top ? e : 0xffffffffu);
+#pragma unroll
+    for (int i = 0; i < MOE_EMAX / 32; ++i)
+      if (best == (uint32_t)(i * 32 + lane)) key[i] = 0u;
+    const float ex = expf(logit[best] - mx);
+    sel += ex;
+    if (lane == j) { mine = ex; chosen = (int)best; }
+  }
+  if (lane < p.top_k) {
+    p.idx[t * p.top_k + lane] = chosen;
+    p.wts[t * p.top_k + lane] = __fdiv_rn(mine, p.renorm ? sel : all);
+  }
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -228,27 +203,20 @@ size_t moe_workspace_bytes(int T, int K, int I, int E, int top_k) {
 }
 
 cudaError_t launch_moe(const MoeLaunch& a, cudaStream_t st) {
-  MoeParams p{};
-  p.x = a.x; p.router = a.router; p.rot = a.rot;
-  p.w1 = a.w1; p.w1_sf = a.w1_sf; p.w2 = a.w2; p.w2_sf = a.w2_sf;
-  p.idx = a.idx; p.wts = a.wts; p.Y = a.Y;
-  p.T = a.T; p.K = a.K; p.I = a.I; p.E = a.E; p.top_k = a.top_k; p.renorm = a.renorm;
-  p.block = a.block; p.block2 = a.block2; p.out_fp32 = a.out_fp32;
-  p.inv_sqrt_b = a.inv_sqrt_b; p.inv_sqrt_b2 = a.inv_sqrt_b2;
-  p.status = a.status;
-  const int A = a.E < a.T * a.top_k ? a.E : a.T * a.top_k;
-  uint8_t* ws = a.ws;
-  p.xq = ws;
-  p.xq_sf = p.xq + up256((size_t)a.T * (a.K / 2));
-  p.hq = p.xq_sf + up256(mx_sf_bytes(a.T, a.K));
-  p.hq_sf = p.hq + up256((size_t)A * a.T * (a.I / 2));
-  const int smem = a.K * 4;
-  cudaError_t e = cudaFuncSetAttribute(moe_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int active = a.E < a.T * a.top_k ? a.E : a.T * a.top_k;
+  uint8_t* xq = a.ws;
+  uint8_t* xq_sf = xq + up256((size_t)a.T * (a.K / 2));
+  uint8_t* hq = xq_sf + up256(mx_sf_bytes(a.T, a.K));
+  uint8_t* hq_sf = hq + up256((size_t)active * a.T * (a.I / 2));
+  PrepParams p{};
+  p.x = a.x; p.router = a.router; p.rot = a.rot; p.idx = a.idx; p.wts = a.wts;
+  p.xq = xq; p.xq_sf = xq_sf;
+  p.T = a.T; p.K = a.K; p.E = a.E; p.top_k = a.top_k; p.renorm = a.renorm; p.block = a.block;
+  p.inv_sqrt_b = a.inv_sqrt_b;
+  moe_route_kernel<<<a.T * PREP_CLUSTER, PREP_THREADS, (size_t)a.K * 2, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  moe_prep_kernel<<<a.T, PREP_THREADS, smem, st>>>(p);
-  moe_gate_up_kernel<<<dim3(A, a.I / 128), 256, 0, st>>>(p);
-  moe_down_kernel<<<dim3((a.K + 127) / 128, a.T), 128, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_moe_products(a, xq, xq_sf, hq, hq_sf, active, st);
 }
 
 }  // namespace rq

@@ -1,0 +1,529 @@
+// MXFP4 products with few tokens: the weights on the tensor core's M side.
+//
+// With T <= 64 tokens a product is bound by reading its weights once (17/32 of
+// a byte each).  A tile of tokens x weights with the tokens on the M side would
+// waste 128 - T of its rows and leave N / 256 CTAs to read everything; here 128
+// weight rows are the M side of tcgen05.mma kind::mxf4 and the tokens its N
+// (16, 32, 48 or 64), and the contraction is split over the CTAs of a cluster,
+// which join their FP32 partial sums through distributed shared memory, always
+// in rank order.
+//
+// One mainloop, three uses:
+//   LINEAR   Y[t, n] = sum_k W[n, k] x[t, k] (+ c L^T)
+//   GATE_UP  one active expert and 128 hidden channels per cluster: two
+//            accumulators (gate rows, up rows); h = w silu(g) u, the block
+//            Hadamard transform and the MXFP4 quantization of the hidden rows in
+//            the epilogue, where the 128 channels of a token are one warp's
+//   DOWN     the contraction runs over all active experts one after another;
+//            hidden rows of tokens that did not choose an expert are zeros, so
+//            the sum over a token's experts happens in the accumulator
+//
+// Per CTA: warp 0 issues the copies (weights and tokens by TMA, 256 columns =
+// 128 bytes a row per stage; scale tiles by bulk copies), warp 1 moves the
+// scales to TMEM and issues the MMAs, warps 4-7 drain the accumulator, all
+// warps do the epilogue.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+
+#include "rq_internal.h"
+#include "rq_mx.cuh"
+#include "rq_ptx.cuh"
+
+namespace rq {
+
+namespace {
+
+constexpr int FEW_THREADS = 256;
+constexpr int FEW_MAX_STAGES = 8;
+constexpr int FEW_PITCH = 132;          // floats between tokens of the partial sums (16-byte rows, no bank repeats)
+constexpr int FEW_TAIL = 1024;          // barriers, TMEM address, active experts
+
+struct __align__(64) FewMaps {
+  CUtensorMap w;   // weight codes, all experts' rows one after another
+  CUtensorMap x;   // token codes
+};
+
+struct FewParams {
+  int T, NT;               // tokens; the MMA's N, T rounded up to 16
+  int K;                   // contraction length (of one expert)
+  int N;                   // output rows (LINEAR, DOWN) or hidden channels I (GATE_UP)
+  int stages;
+  int tail;                // offset of the barriers, behind the stages
+  uint32_t tmem_cols;
+  int early;               // weights may be read before the previous kernel has finished
+  const uint8_t* w_sf;     // weight scales: of one expert after another
+  size_t w_sf_expert;      // bytes of one expert's scales
+  const uint8_t* x_sf;     // token scales (DOWN: one buffer per active expert)
+  const int32_t* idx;      // T x top_k chosen experts
+  const float* wts;
+  int top_k;
+  const uint16_t *c, *L;   // low-rank branch (LINEAR)
+  int r;
+  void* Y;
+  int out_fp32;
+  uint8_t *hq, *hq_sf;     // hidden rows out (GATE_UP)
+  int block2;
+  float inv_sqrt_b2;
+  int32_t* status;
+  uint64_t wait_ns;
+  uint32_t inject_tx;
+};
+
+__device__ __forceinline__ uint32_t few_mapa(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 few_ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void few_tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Ascending list of the experts that some token chose, in act[]; its length.
+// bits: 8 words of shared scratch.  Called by the whole CTA.
+__device__ int list_active(const int32_t* idx, int n, uint32_t* bits, uint16_t* act) {
+  if (threadIdx.x < 8) bits[threadIdx.x] = 0u;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += FEW_THREADS) {
+    const uint32_t e = (uint32_t)__ldcg(idx + i) & 255u;
+    atomicOr(&bits[e >> 5], 1u << (e & 31));
+  }
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = __popc(bits[i]);
+    before += i < ((int)threadIdx.x >> 5) ? c : 0;
+    all += c;
+  }
+  const uint32_t w = bits[threadIdx.x >> 5], lane = threadIdx.x & 31;   // 256 threads, one expert each
+  if (w >> lane & 1u) act[before + __popc(w & ((1u << lane) - 1u))] = (uint16_t)threadIdx.x;
+  __syncthreads();
+  return all;
+}
+
+// E2M1 x E2M1, E8M0 scales per 32, N = n; a 64-wide instruction takes bytes
+// id, id + 1 of each scale word.
+__device__ __forceinline__ uint32_t few_idesc(int n, uint32_t id) {
+  return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (8u << 24) | (id << 29);
+}
+
+enum { LINEAR = 0, GATE_UP = 1, DOWN = 2 };
+
+template <int MODE>
+__global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_constant__ FewMaps tm,
+                                                                const __grid_constant__ FewParams p) {
+  constexpr int NA = MODE == GATE_UP ? 2 : 1;
+  constexpr int PA = 128 * 128, SF = 1024;            // weight codes, scales of 128 rows per stage
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  const int PB = p.NT * 128;
+  const int STAGE = NA * (PA + SF) + PB + SF;
+  // stage: [NA] weight codes | token codes | [NA] weight scales | token scales
+  uint8_t* tail = smem + p.tail;
+  uint64_t* full = reinterpret_cast<uint64_t*>(tail);
+  uint64_t* empty = full + FEW_MAX_STAGES;
+  uint64_t* accfull = empty + FEW_MAX_STAGES;
+  uint64_t* mdrain = accfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
+  uint32_t* bits = tmem_slot + 4;
+  uint16_t* act = reinterpret_cast<uint16_t*>(bits + 8);
+  float* part = reinterpret_cast<float*>(smem);       // [NA][NT][FEW_PITCH], over the stages once they are used up
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  uint32_t S;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+  const int tile = (int)(blockIdx.x / S), n0 = tile * 128;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    mbar_init(accfull, 1);
+    mbar_init(mdrain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm.w);
+    prefetch_tmap(&tm.x);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (!p.early) griddep_wait();
+
+  // this rank's steps of 256 columns: [s0, s0 + n)
+  const int spe = (p.K + 255) / 256, KT = (p.K + 127) / 128;
+  int total = spe, expert = 0;
+  bool live = true;
+  if constexpr (MODE != LINEAR) {
+    const int na = list_active(p.idx, p.T * p.top_k, bits, act);
+    if constexpr (MODE == GATE_UP) {
+      griddep_launch_dependents();   // every CTA of this grid has seen the routing by now
+      live = (int)blockIdx.y < na;
+      if (live) expert = act[blockIdx.y];
+    } else {
+      total = na * spe;
+    }
+  }
+  const int s0 = (int)((int64_t)total * rank / S);
+  const int n = live ? (int)((int64_t)total * (rank + 1) / S) - s0 : 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const size_t rowt = (size_t)(n0 / 128) * KT * 512;   // this row tile's scales
+      auto load = [&](int i, bool wt, bool tk) {
+        const int st = s0 + i, a = MODE == DOWN ? st / spe : 0, kt = MODE == DOWN ? st - a * spe : st;
+        const int e = MODE == DOWN ? act[a] : expert;
+        uint64_t* bar = &full[i % p.stages];
+        uint8_t* s = smem + (i % p.stages) * STAGE;
+        const uint32_t sfb = (uint32_t)min(2, KT - kt * 2) * 512;   // scale bytes of 128 rows
+        if (wt) {
+          mbar_expect_tx(bar, NA * (PA + sfb) + PB + sfb + (i == 0 ? p.inject_tx : 0u));
+          const uint8_t* sf = p.w_sf + (MODE == LINEAR ? 0 : (size_t)e * p.w_sf_expert) + (size_t)kt * 1024;
+#pragma unroll
+          for (int h = 0; h < NA; ++h) {   // GATE_UP: rows I..2I-1 are the up rows
+            const int row = (MODE == LINEAR ? 0 : e * NA * p.N) + h * p.N + n0;
+            tma_load_2d(s + h * PA, &tm.w, kt * 128, row, bar);
+            bulk_g2s(s + NA * PA + PB + h * SF, sf + (size_t)h * (p.N / 128) * KT * 512 + rowt, sfb, bar);
+          }
+        }
+        if (tk) {
+          tma_load_2d(s + NA * PA, &tm.x, kt * 128, a * p.T, bar);
+          bulk_g2s(s + NA * (PA + SF) + PB, p.x_sf + (size_t)a * KT * 512 + (size_t)kt * 1024, sfb, bar);
+        }
+      };
+      int i = 0;
+      if (p.early) {   // the first stages' weights now, their tokens once the previous kernel is done
+        const int head = min(n, p.stages);
+        for (int j = 0; j < head; ++j) load(j, true, false);
+        griddep_wait();
+        for (; i < head; ++i) load(i, false, true);
+      }
+      for (; i < n; ++i) {
+        if (i >= p.stages &&
+            !mbar_wait(&empty[i % p.stages], ((i / p.stages) - 1) & 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns))
+          break;
+        load(i, true, true);
+      }
+      if (*abort_flag)   // let the copies already issued land (bounded)
+        for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j) mbar_drain(&full[j % p.stages], (j / p.stages) & 1, p.wait_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && n > 0) {
+      bool ok = true;
+      for (int i = 0; i < n; ++i) {
+        const int s = i % p.stages;
+        ok = mbar_wait(&full[s], (i / p.stages) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+        if (!ok) break;
+        tc_fence_after();
+        const int kt = MODE == DOWN ? (s0 + i) % spe : s0 + i;
+        const int sct = min(2, KT - kt * 2), kkn = min(4, p.K / 64 - kt * 4);
+        const uint32_t st = sbase + s * STAGE;
+        // a slot of scale columns per stage: free again when the stage is
+        const uint32_t tsf = tmem + NA * p.NT + s * (NA + 1) * 8;
+        for (int q = 0; q < sct; ++q) {
+#pragma unroll
+          for (int h = 0; h <= NA; ++h)   // weight scales, then the tokens'
+            tc_cp_32x128b_warpx4(tsf + h * 8 + q * 4, smem_desc(st + NA * PA + PB + h * SF + q * 512, 16, 128, 0));
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < kkn) {
+#pragma unroll
+            for (int h = 0; h < NA; ++h)
+              umma_mxf4(tmem + h * p.NT, smem_desc(st + h * PA + kk * 32, 16, 1024, 2),
+                        smem_desc(st + NA * PA + kk * 32, 16, 1024, 2), few_idesc(p.NT, (kk & 1) * 2),
+                        tsf + h * 8 + (kk >> 1) * 4, tsf + NA * 8 + (kk >> 1) * 4, i > 0 || kk > 0);
+          }
+        tc_commit(&empty[s]);
+      }
+      if (ok) {
+        tc_commit(accfull);
+      } else {   // wait (bounded) for the MMAs already issued
+        tc_commit(mdrain);
+        mbar_drain(mdrain, 0, p.wait_ns);
+      }
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3;
+    const bool ok = n > 0 && mbar_wait(accfull, 0, p.status, ST_TIMEOUT_MMA, abort_flag, p.wait_ns);
+    if (ok) tc_fence_after();
+    for (int c = 0; c < NA * p.NT; c += 16) {
+      uint32_t v[16];
+      if (ok) {
+        few_tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+        tmem_ld_wait();
+      } else {   // no steps fell to this rank
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = 0u;
+      }
+      if (ok || n == 0) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * FEW_PITCH + q * 32 + lane] = __uint_as_float(v[j]);
+      }
+    }
+    tc_fence_before();
+  }
+  if (p.early) griddep_wait();   // nothing is written before the previous kernel is done
+  __syncwarp();
+  if (S > 1) cluster_sync();
+  else __syncthreads();
+
+  // ------------------------------------------------------------ join and epilogue
+  // token t belongs to rank t % S, a warp per token, four rows per lane
+  if (live) {
+    const uint32_t mine = sbase + lane * 16;
+    auto sum = [&](int row) {
+      float4 v = few_ld_cluster(few_mapa(mine + row * FEW_PITCH * 4, 0));
+      for (uint32_t s = 1; s < S; ++s) {
+        const float4 w = few_ld_cluster(few_mapa(mine + row * FEW_PITCH * 4, s));
+        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+      }
+      return v;
+    };
+    for (int t = (int)rank + warp * (int)S; t < p.T; t += (int)S * (FEW_THREADS / 32)) {
+      if constexpr (MODE == GATE_UP) {
+        // the token's weight for this expert, if it chose it
+        const bool hit = lane < p.top_k && __ldcg(p.idx + t * p.top_k + min(lane, p.top_k - 1)) == expert;
+        const uint32_t who = __ballot_sync(0xffffffffu, hit);
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (who) {
+          const float w = __ldcg(p.wts + t * p.top_k + __ffs(who) - 1);
+          const float4 g = sum(t), u = sum(p.NT + t);
+          const float gg[4] = {g.x, g.y, g.z, g.w}, uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = __fmul_rn(w, __fmul_rn(__fdiv_rn(gg[i], __fadd_rn(1.f, expf(-gg[i]))), uu[i]));
+          // channels 4 lane .. 4 lane + 3: strides 1 and 2 here, 4 .. across lanes
+          float a = v[0], b = v[2];
+          v[0] = __fadd_rn(a, v[1]); v[1] = __fsub_rn(a, v[1]);
+          v[2] = __fadd_rn(b, v[3]); v[3] = __fsub_rn(b, v[3]);
+          a = v[0]; b = v[1];
+          v[0] = __fadd_rn(a, v[2]); v[2] = __fsub_rn(a, v[2]);
+          v[1] = __fadd_rn(b, v[3]); v[3] = __fsub_rn(b, v[3]);
+          for (int m = 1; m < p.block2 / 4; m <<= 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float o = __shfl_xor_sync(0xffffffffu, v[i], m);
+              v[i] = lane & m ? __fsub_rn(o, v[i]) : __fadd_rn(v[i], o);
+            }
+          }
+        }
+        float am = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = __fmul_rn(v[i], p.inv_sqrt_b2);
+          am = fmax_nan(am, fabsf(v[i]));
+        }
+#pragma unroll
+        for (int m = 1; m < 8; m <<= 1) am = fmax_nan(am, __shfl_xor_sync(0xffffffffu, am, m));
+        const uint32_t sb = mx_scale_byte(am);
+        const float inv = mx_inv_scale(sb);
+        const uint32_t lo = cvt_e2m1x2(__fmul_rn(v[1], inv), __fmul_rn(v[0], inv));
+        const uint32_t hi = cvt_e2m1x2(__fmul_rn(v[3], inv), __fmul_rn(v[2], inv));
+        const size_t row = (size_t)blockIdx.y * p.T + t;
+        reinterpret_cast<uint16_t*>(p.hq)[(row * (p.N / 2) + n0 / 2) / 2 + lane] =
+            sb == 255u ? (uint16_t)0 : (uint16_t)(lo | hi << 8);
+        if ((lane & 7) == 0)
+          p.hq_sf[(size_t)blockIdx.y * (p.N / 128) * 512 + mx_sf_offset(t, n0 / 32 + lane / 8, p.N)] = (uint8_t)sb;
+      } else {
+        float4 y = sum(t);
+        float v[4] = {y.x, y.y, y.z, y.w};
+        const int nn = n0 + 4 * lane;
+        if constexpr (MODE == LINEAR) {
+          if (p.c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float s = 0.f;
+              if (nn + i < p.N)
+                for (int j = 0; j < p.r; ++j)
+                  s = fmaf(bf16_bits_to_f32(p.c[(size_t)t * p.r + j]), bf16_bits_to_f32(p.L[(size_t)(nn + i) * p.r + j]), s);
+              v[i] += s;
+            }
+          }
+        }
+        const size_t at = (size_t)t * p.N + nn;
+        if (p.out_fp32) {
+          float* out = static_cast<float*>(p.Y) + at;
+          if (nn + 4 <= p.N && (p.N & 3) == 0) {
+            *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (nn + i < p.N) out[i] = v[i];
+          }
+        } else {
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.Y) + at;
+          if (nn + 4 <= p.N && (p.N & 3) == 0) {
+            const __nv_bfloat162 b0 = __floats2bfloat162_rn(v[0], v[1]), b1 = __floats2bfloat162_rn(v[2], v[3]);
+            *reinterpret_cast<uint2*>(out) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (nn + i < p.N) out[i] = __float2bfloat16_rn(v[i]);
+          }
+        }
+      }
+    }
+  }
+  // the partial sums stay until every rank has read them
+  if (S > 1) cluster_sync();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn find_encode() {
+  void* f = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess)
+    return reinterpret_cast<EncodeTiledFn>(f);
+  return nullptr;
+}
+
+// rows x cols/2 bytes of packed codes in boxes of 128 bytes x `box` rows
+bool code_map(CUtensorMap* m, const uint8_t* codes, uint64_t rows, uint64_t cols, uint32_t box) {
+  static const EncodeTiledFn enc = find_encode();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {cols / 2, rows}, strides[1] = {cols / 2};
+  cuuint32_t b[2] = {128, box}, es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, b, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The dynamic shared memory limit is raised once per kernel and device.
+template <class Kern>
+cudaError_t allow_smem(Kern k, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (done.load() >> (dev & 63) & 1u)) return e;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+  return e;
+}
+
+// `tiles` x `ny` clusters, `steps` K steps to split.
+template <int MODE>
+cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int steps, int sms, cudaStream_t st) {
+  constexpr int NA = MODE == GATE_UP ? 2 : 1;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(mx_few_kernel<MODE>, done);
+  if (e != cudaSuccess) return e;
+  // ranks per cluster: the fewest that give every SM a CTA, two steps each at least
+  int S = 1;
+  while (S < 8 && (int64_t)tiles * ny * S < sms && 4 * S <= steps) S *= 2;
+  const int stage = NA * (128 * 128 + 1024) + p.NT * 128 + 1024;
+  const int parts = (NA * p.NT * FEW_PITCH * 4 + 1023) & ~1023;   // the partial sums overlay the stages
+  // one CTA per SM: shared memory full of stages; more of them: two share an SM
+  const int limit = (int64_t)tiles * ny * S > sms ? 115712 : 230400;
+  p.stages = (limit - FEW_TAIL - 1024) / stage;
+  if (p.stages > FEW_MAX_STAGES) p.stages = FEW_MAX_STAGES;
+  const int most = (steps + S - 1) / S;
+  if (p.stages > most) p.stages = most < 1 ? 1 : most;
+  p.tail = p.stages * stage > parts ? p.stages * stage : parts;
+  uint32_t cols = 32;
+  while ((int)cols < NA * p.NT + p.stages * (NA + 1) * 8) cols *= 2;
+  p.tmem_cols = cols;
+  // shared memory is taken in at least the proportion of TMEM (of 228 KB, 1 KB
+  // of it the system's per CTA): CTAs that share an SM by the one fit by the
+  // other, so that no allocation waits for a CTA that waits for its cluster
+  int smem = p.tail + FEW_TAIL + 1024;
+  const int share = (int)cols * 456 - 1024;
+  if (smem < share) smem = share;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)S;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * S), (unsigned)ny);
+  cfg.blockDim = dim3(FEW_THREADS);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, mx_few_kernel<MODE>, tm, p);
+}
+
+int token_columns(int T) { return (T + 15) / 16 * 16; }
+
+}  // namespace
+
+cudaError_t launch_mx_few(const GemmLaunch& a, cudaStream_t st, const char** why) {
+  FewMaps tm;
+  FewParams p{};
+  p.T = a.M; p.NT = token_columns(a.M); p.K = a.K; p.N = a.N;
+  p.early = a.early_weights;
+  p.w_sf = a.w_bscale; p.x_sf = a.a_bscale;
+  p.c = a.c; p.L = a.L; p.r = a.r;
+  p.Y = a.Y; p.out_fp32 = a.out_fp32;
+  p.status = a.status; p.wait_ns = a.wait_ns; p.inject_tx = a.inject_tx;
+  if (!code_map(&tm.w, a.w_codes, a.N, a.K, 128) || !code_map(&tm.x, a.a_codes, a.M, a.K, p.NT)) {
+    *why = "cuTensorMapEncodeTiled failed";
+    return cudaErrorInvalidValue;
+  }
+  return launch_mode<LINEAR>(tm, p, (a.N + 127) / 128, 1, (a.K + 255) / 256, a.num_sms > 0 ? a.num_sms : 148, st);
+}
+
+cudaError_t launch_moe_products(const MoeLaunch& a, const uint8_t* xq, const uint8_t* xq_sf, uint8_t* hq, uint8_t* hq_sf,
+                                int active, cudaStream_t st) {
+  const int sms = a.num_sms > 0 ? a.num_sms : 148;
+  FewMaps tm;
+  FewParams p{};
+  p.T = a.T; p.NT = token_columns(a.T); p.K = a.K; p.N = a.I;
+  p.w_sf = a.w1_sf; p.w_sf_expert = mx_sf_bytes(2 * a.I, a.K);
+  p.x_sf = xq_sf;
+  p.idx = a.idx; p.wts = a.wts; p.top_k = a.top_k;
+  p.hq = hq; p.hq_sf = hq_sf; p.block2 = a.block2; p.inv_sqrt_b2 = a.inv_sqrt_b2;
+  p.status = a.status; p.wait_ns = a.wait_ns; p.inject_tx = a.inject_tx;
+  if (!code_map(&tm.w, a.w1, (uint64_t)a.E * 2 * a.I, a.K, 128) || !code_map(&tm.x, xq, a.T, a.K, p.NT))
+    return cudaErrorInvalidValue;
+  cudaError_t e = launch_mode<GATE_UP>(tm, p, a.I / 128, active, (a.K + 255) / 256, sms, st);
+  if (e != cudaSuccess) return e;
+  p.K = a.I; p.N = a.K;
+  p.early = 1;   // the routing was complete before the gate/up kernel let this one start
+  p.w_sf = a.w2_sf; p.w_sf_expert = mx_sf_bytes(a.K, a.I);
+  p.x_sf = hq_sf;
+  p.Y = a.Y; p.out_fp32 = a.out_fp32;
+  if (!code_map(&tm.w, a.w2, (uint64_t)a.E * a.K, a.I, 128) ||
+      !code_map(&tm.x, hq, (uint64_t)active * a.T, a.I, p.NT))
+    return cudaErrorInvalidValue;
+  return launch_mode<DOWN>(tm, p, (a.K + 127) / 128, 1, active * ((a.I + 255) / 256), sms, st);
+}
+
+}  // namespace rq

@@ -676,3 +676,47 @@ def test_quantized_layers_together(L):
             g[t] += float(w[t, j]) * (W2[e * K:(e + 1) * K] @ (gu[:I] * torch.sigmoid(gu[:I]) * gu[I:]))
     assert rel(y, g) < 0.5
     assert rel(z, y.double() @ Wa.T) < 0.25
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 64, 200])
+def test_layer_wait_runs_out_then_recovers(L, M):
+    # the test hook overstates the first copies' bytes: the bounded waits run
+    # out, the call reports it, and the next call is right again
+    N, K = 300, 1024
+    X, rot_t, wc, wsf, A, B = _layer_case(M, N, K, 128)
+    ws, st = _workspace(rq.rq_mxfp4_layer_workspace(M, N, K)), _status()
+    Y0, Y = (torch.empty((M, N), device="cuda") for _ in range(2))
+    rq.rq_mxfp4_layer(X, 128, rot_t, wc, wsf, ws, Y0, 1, st)
+    _ok(st)
+    rq.rq_set_wait_limit(5_000_000)
+    rq.rq_set_fault_injection(16)
+    try:
+        rq.rq_mxfp4_layer(X, 128, rot_t, wc, wsf, ws, Y, 1, st)
+        rc, code = rq.rq_read_status(st)
+    finally:
+        rq.rq_set_fault_injection(0)
+        rq.rq_set_wait_limit(0)
+    assert rc == 5 and code in {0x101, 0x102, 0x103, 0x104, 0x105}
+    st.zero_()
+    rq.rq_mxfp4_layer(X, 128, rot_t, wc, wsf, ws, Y, 1, st)
+    _ok(st)
+    assert torch.equal(Y, Y0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 40])
+def test_moe_wait_runs_out_then_recovers(L, T):
+    m, st = Moe(T, 256, 256, 8, 2, True, 64, 64), _status()
+    _, _, Y0 = m.run()
+    rq.rq_set_wait_limit(5_000_000)
+    rq.rq_set_fault_injection(16)
+    try:
+        m.run(st=st)
+        rc, code = rq.rq_read_status(st)
+    finally:
+        rq.rq_set_fault_injection(0)
+        rq.rq_set_wait_limit(0)
+    assert rc == 5 and code in {0x101, 0x102, 0x103, 0x104, 0x105}
+    _, _, Y = m.run()
+    assert torch.equal(Y, Y0)
