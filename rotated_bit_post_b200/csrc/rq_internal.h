@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #define RQ_FMT_INT4 1
@@ -91,6 +92,22 @@ struct PcaLaunch {
 
 cudaError_t launch_pca(const PcaLaunch& a, cudaStream_t st);
 
+// Raises a kernel's dynamic shared memory limit to the most a CTA can have,
+// once per device.
+struct SmemLimit {
+  std::atomic<uint64_t> done{0};
+  cudaError_t raise(const void* kernel) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1u))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+    return e;
+  }
+};
+
+// MXFP4 rows with one rotation and no low-rank branch (rq_mx.cu)
+cudaError_t launch_mx_quantize(const K1Launch& a, cudaStream_t st);
 // MXFP4 codes -> values
 struct MxDequantLaunch {
   const uint8_t* codes;

@@ -836,7 +836,8 @@ cudaError_t launch_k1_fmt(const K1Launch& a, cudaStream_t st) {
     case RQ_FMT_LM16: return launch_k1_mode<L, RQ_FMT_LM16>(a, st);
     case RQ_FMT_LM4: return launch_k1_mode<L, RQ_FMT_LM4>(a, st);
     case RQ_FMT_NVFP4: return launch_k1_mode<L, RQ_FMT_NVFP4>(a, st);
-    case RQ_FMT_MXFP4: return launch_k1_mode<L, RQ_FMT_MXFP4>(a, st);
+    case RQ_FMT_MXFP4:   // rows without the projection run in rq_mx.cu
+      return a.weight ? launch_k1_ipw<L, RQ_FMT_MXFP4, true, true>(a, st) : launch_k1_ipw<L, RQ_FMT_MXFP4, true, false>(a, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -844,6 +845,7 @@ cudaError_t launch_k1_fmt(const K1Launch& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_k1(const K1Launch& a, cudaStream_t st) {
+  if (a.fmt == RQ_FMT_MXFP4 && !a.U && !a.rot2) return launch_mx_quantize(a, st);
   // the rows-as-lanes kernel: for what only it does (double rotation, INT4A,
   // INT8, the weight code sums, blocks outside 128-512, K an odd multiple of
   // 64) and where its layout pays: whole rows of 32

@@ -162,9 +162,8 @@ struct SqTree {
 
 template <int FMT, bool WEIGHT, int B, int SEG>
 __global__ void __launch_bounds__(R_THREADS, 1) k1r_kernel(const __grid_constant__ K1RParams p) {
-  static_assert(SEG == 128 || (B <= 64 && (FMT == RQ_FMT_LM16 || FMT == RQ_FMT_LM4 || FMT == RQ_FMT_NVFP4 ||
-                                            FMT == RQ_FMT_MXFP4)),
-                "64-wide segments carry codebook, NVFP4 and MXFP4 rows with blocks up to 64");
+  static_assert(SEG == 128 || (B <= 64 && (FMT == RQ_FMT_LM16 || FMT == RQ_FMT_LM4 || FMT == RQ_FMT_NVFP4)),
+                "64-wide segments carry codebook and NVFP4 rows with blocks up to 64");
   constexpr int TS = SEG + 4;
   constexpr int T = B > SEG ? B / SEG : 1;        // threads per Hadamard block (<= F)
   const int F = p.F;
@@ -547,9 +546,7 @@ __global__ void __launch_bounds__(R_THREADS, 1) k1r_kernel(const __grid_constant
 #pragma unroll
       for (int c = 0; c < SEG / 32; ++c) dst[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       // the segment's scale bytes are adjacent in the tile layout
-      uint8_t* sf = p.bscale + mx_sf_offset(row, seg * (SEG / 32), K);
-      if constexpr (SEG == 128) *reinterpret_cast<uint32_t*>(sf) = sbw;
-      else *reinterpret_cast<uint16_t*>(sf) = (uint16_t)sbw;
+      *reinterpret_cast<uint32_t*>(p.bscale + mx_sf_offset(row, seg * (SEG / 32), K)) = sbw;
     } else {   // NVFP4: SEG / 16 groups of 16 elements
       uint32_t pk[SEG / 8];
       uint32_t sbw[2] = {0u, 0u};
@@ -708,9 +705,9 @@ cudaError_t launch_r(const K1Launch& a, cudaStream_t st) {
 bool k1r_supports(const K1Launch& a) {
   if (a.U) return false;
   if (a.K % 64) return false;
-  // 64-wide segments: codebook, NVFP4 and MXFP4 codes with blocks up to 64, one rotation
+  // 64-wide segments: codebook and NVFP4 codes with blocks up to 64, one rotation
   if (a.K % 128 && (a.block > 64 || a.rot2 || a.wz ||
-                    (a.fmt != RQ_FMT_LM16 && a.fmt != RQ_FMT_LM4 && a.fmt != RQ_FMT_NVFP4 && a.fmt != RQ_FMT_MXFP4)))
+                    (a.fmt != RQ_FMT_LM16 && a.fmt != RQ_FMT_LM4 && a.fmt != RQ_FMT_NVFP4)))
     return false;
   if (a.rot2 && a.K > 8192) return false;   // the FP32 row copy of the double rotation
   switch (a.block) {
@@ -728,7 +725,6 @@ cudaError_t launch_r_t64(const K1Launch& a, cudaStream_t st) {
       case RQ_FMT_LM16: return a.weight ? launch_r<RQ_FMT_LM16, true, BS, 64>(a, st) : launch_r<RQ_FMT_LM16, false, BS, 64>(a, st);
       case RQ_FMT_LM4: return a.weight ? launch_r<RQ_FMT_LM4, true, BS, 64>(a, st) : cudaErrorInvalidValue;
       case RQ_FMT_NVFP4: return a.weight ? launch_r<RQ_FMT_NVFP4, true, BS, 64>(a, st) : launch_r<RQ_FMT_NVFP4, false, BS, 64>(a, st);
-      case RQ_FMT_MXFP4: return launch_r<RQ_FMT_MXFP4, false, BS, 64>(a, st);
     }
   }
   return cudaErrorInvalidValue;
@@ -737,7 +733,8 @@ cudaError_t launch_r_t64(const K1Launch& a, cudaStream_t st) {
 template <int BS>
 cudaError_t launch_r_t(const K1Launch& a, cudaStream_t st) {
   if (a.K % 128) return launch_r_t64<BS>(a, st);
-  if (a.fmt == RQ_FMT_MXFP4) return launch_r<RQ_FMT_MXFP4, false, BS, 128>(a, st);   // the same for both sides
+  // MXFP4 comes here for the double rotation; activations and weight rows alike
+  if (a.fmt == RQ_FMT_MXFP4) return launch_r<RQ_FMT_MXFP4, false, BS, 128>(a, st);
   if (a.weight) {
     switch (a.fmt) {
       case RQ_FMT_INT4: return launch_r<RQ_FMT_INT4, true, BS, 128>(a, st);

@@ -1,4 +1,9 @@
-// MXFP4 codes read back as the values they stand for.
+// MXFP4: the activation (and weight-row) transform, rotate -> quantize -> pack,
+// and codes read back as values.
+//
+// MXFP4 has no row scale: a block of 32 rotated coordinates is quantized from
+// its own maximum, so one pass over the transformed values in registers is
+// all there is, and no thread waits for a row's other blocks.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -6,36 +11,342 @@
 
 #include "rq_internal.h"
 #include "rq_mx.cuh"
+#include "rq_ptx.cuh"
 
 namespace rq {
 
 namespace {
 
-// One thread per 8 codes: a 4-byte read, a scale byte, 8 values out.
+// ------------------------------------------------------------ rotate + quantize
+// Persistent over groups of R rows (1, 2, 4 or 8), two groups in flight: a group's
+// rows land in shared memory by bulk copies, at a pitch that puts the R rows
+// 128 / R bytes apart modulo the banks.  A warp's lanes are R rows x 32 / R
+// segments of 64 rotated coordinates; a thread gathers its segment through the
+// signed-permutation table (16 bits per coordinate: byte offset, sign in bit
+// 15), two chunks of 32 that are one MXFP4 block each.
+// Butterflies: strides 1 .. 16 inside the chunks, 32 between the two chunks,
+// 64 between the chunks after one of them was exchanged with the neighbouring
+// segment's (half the shuffles of a butterfly across lanes), 128 and up across
+// lanes.  For the exchange the odd segment holds its chunks in reverse, so that
+// every lane sends and receives its second chunk; the signs that this turns
+// round are +-1 factors of the packed multiply-adds, exact.
+constexpr int MXQ_THREADS = 512;
+
+struct MxqParams {
+  const uint16_t* x;
+  const int32_t* rot;
+  uint8_t* codes;
+  uint8_t* sf;
+  int32_t* status;
+  uint64_t wait_ns;
+  uint32_t inject_tx;
+  int rows, K, block, lr;   // lr: log2 of the rows per group
+  int ngroups;
+  float isb;                // fp32(1 / sqrt(block))
+};
+
+constexpr int MXQ_SEG = 144;   // bytes of a segment's table entries: 64 x 2, and 16 that shift the banks
+
+// (p, q) of two values each -> (s p + q, p - s q), s = +-1
+__device__ __forceinline__ void cross2(float& p0, float& p1, float& q0, float& q1, float s) {
+  asm("{\n\t.reg .b64 p, q, s, n, a;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmov.b64 n, {%5, %5};\n\t"
+      "fma.rn.f32x2 a, s, p, q;\n\tfma.rn.f32x2 q, n, q, p;\n\t"
+      "mov.b64 {%0, %1}, a;\n\tmov.b64 {%2, %3}, q;\n\t}"
+      : "+f"(p0), "+f"(p1), "+f"(q0), "+f"(q1)
+      : "f"(s), "f"(-s));
+}
+__device__ __forceinline__ void bfly2(float& a0, float& a1, float& b0, float& b1) {
+  asm("{\n\t.reg .b64 a, b, s, d;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 s, a, b;\n\tsub.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, s;\n\tmov.b64 {%2, %3}, d;\n\t}"
+      : "+f"(a0), "+f"(a1), "+f"(b0), "+f"(b1));
+}
+// v = s v + o on two values, s = +-1
+__device__ __forceinline__ void sfma2(float& v0, float& v1, float s, float o0, float o1) {
+  asm("{\n\t.reg .b64 v, o, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 o, {%3, %4};\n\tmov.b64 s, {%2, %2};\n\t"
+      "fma.rn.f32x2 v, s, v, o;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(v0), "+f"(v1)
+      : "f"(s), "f"(o0), "f"(o1));
+}
+__device__ __forceinline__ void mul2(float& v0, float& v1, float s) {
+  asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\t"
+      "mul.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(v0), "+f"(v1)
+      : "f"(s));
+}
+// max(|a|, |b|, |c|), NaN if one is
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 32 coordinates of one chunk through the table
+__device__ __forceinline__ void gather32(float (&v)[32], const uint8_t* row, const uint8_t* tab) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 t = *reinterpret_cast<const uint4*>(tab + 16 * j);
+    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = w[i], b = w[i] >> 16;
+      const uint32_t xa = *reinterpret_cast<const uint16_t*>(row + (a & 0x7FFEu));
+      const uint32_t xb = *reinterpret_cast<const uint16_t*>(row + (b & 0x7FFEu));
+      v[8 * j + 2 * i] = __uint_as_float((xa ^ (a & 0x8000u)) << 16);
+      v[8 * j + 2 * i + 1] = __uint_as_float((xb << 16) ^ (w[i] & 0x80000000u));
+    }
+  }
+}
+
+__device__ __forceinline__ void fwht_chunk(float (&v)[32], int block) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const float a = v[e], b = v[e + 1];
+    v[e] = __fadd_rn(a, b);
+    v[e + 1] = __fsub_rn(a, b);
+  }
+#pragma unroll
+  for (int h = 2; h <= 8; h <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2)
+      if ((e & h) == 0) bfly2(v[e], v[e + 1], v[e + h], v[e + h + 1]);
+  }
+  if (block > 16) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) bfly2(v[e], v[e + 1], v[e + 16], v[e + 17]);
+  }
+}
+
+// Scale byte and packed codes of a transformed chunk (before the 1/sqrt(block)).
+// Rounding is monotone, so the largest |y| is that of the largest |v|.  One
+// product by isb 2^(127 - byte) then equals the two roundings of the stated
+// order, (v isb) rounded and scaled exactly, unless something is subnormal:
+// at byte 32 a subnormal y lands below 2^-31 and is 0 either way, and the
+// factor itself is normal up to byte 240; outside both steps are taken.
+__device__ __forceinline__ uint32_t quantize32(float (&v)[32], float isb, uint4& out) {
+  float am = fabsf(v[0]);
+#pragma unroll
+  for (int e = 1; e < 31; e += 2) am = max3_abs(am, v[e], v[e + 1]);
+  am = max3_abs(am, v[31], 0.f);
+  const uint32_t sb = mx_scale_byte(__fmul_rn(am, isb));
+  float f = mx_inv_scale(sb);
+  if (sb < 32u || sb > 240u) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], isb);
+  } else {
+    f *= isb;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w[j] = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      float a = v[8 * j + e], b = v[8 * j + e + 1];
+      mul2(a, b, f);
+      w[j] |= (uint32_t)cvt_e2m1x2(b, a) << (4 * e);
+    }
+    if (sb == 255u) w[j] = 0u;
+  }
+  out = make_uint4(w[0], w[1], w[2], w[3]);
+  return sb;
+}
+
+__global__ void __launch_bounds__(MXQ_THREADS, 1) mx_quantize_kernel(const __grid_constant__ MxqParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int K = p.K, lr = p.lr, R = 1 << lr;
+  const int nseg = K / 64;
+  const int pitch = 2 * K + (lr ? 128 >> lr : 0);
+  uint8_t* tab = smem;
+  uint8_t* rowbuf = smem + nseg * MXQ_SEG;              // [2][R][pitch]
+  uint64_t* full = reinterpret_cast<uint64_t*>(rowbuf + 2 * R * pitch);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(full + 2);
+  const int nthreads = blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = nthreads >> 5;
+
+  auto issue = [&](int g, int buf) {
+    const int r0 = g << lr, nr = min(R, p.rows - r0);
+    mbar_expect_tx(&full[buf], (uint32_t)nr * 2 * K + (g == (int)blockIdx.x ? p.inject_tx : 0u));
+    for (int i = 0; i < nr; ++i)
+      bulk_g2s(rowbuf + (buf * R + i) * pitch, p.x + (size_t)(r0 + i) * K, (uint32_t)(2 * K), &full[buf]);
+  };
+  if (threadIdx.x == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    issue(blockIdx.x, 0);
+    if (blockIdx.x + gridDim.x < p.ngroups) issue(blockIdx.x + gridDim.x, 1);
+    // the product that reads these codes may be scheduled: it waits for this
+    // grid before it reads them
+    griddep_launch_dependents();
+  }
+  for (int i = threadIdx.x; i < K / 4; i += nthreads) {
+    const int4 r = __ldg(reinterpret_cast<const int4*>(p.rot) + i);
+    auto entry = [](int32_t v) { return (uint32_t)(v & 0x3FFF) << 1 | (v < 0 ? 0x8000u : 0u); };
+    *reinterpret_cast<uint2*>(tab + (i / 16) * MXQ_SEG + (i % 16) * 8) =
+        make_uint2(entry(r.x) | entry(r.y) << 16, entry(r.z) | entry(r.w) << 16);
+  }
+  __syncthreads();
+
+  const int spw = 32 >> lr;                              // segments per warp
+  const int rl = lane & (R - 1), sl = lane >> lr;
+  const int nunits = (nseg + spw - 1) / spw;
+  int it = 0;
+  for (int g = blockIdx.x; g < p.ngroups; g += gridDim.x, ++it) {
+    const int buf = it & 1, r0 = g << lr, nr = min(R, p.rows - r0);
+    const bool ok = mbar_wait(&full[buf], (it >> 1) & 1, p.status, ST_TIMEOUT_LOAD, abort_flag, p.wait_ns);
+    for (int u = warp; ok && u < nunits; u += nwarps) {
+      const int seg = u * spw + sl;
+      const bool live = seg < nseg && rl < nr;
+      const bool odd = p.block > 64 && (seg & 1);
+      const uint8_t* t = tab + min(seg, nseg - 1) * MXQ_SEG;
+      const uint8_t* row = rowbuf + (buf * R + rl) * pitch;
+      float a[32], b[32];
+      gather32(a, row, t + (odd ? 64 : 0));
+      gather32(b, row, t + (odd ? 0 : 64));
+      fwht_chunk(a, p.block);
+      fwht_chunk(b, p.block);
+      const float s = odd ? -1.f : 1.f;
+      if (p.block > 32) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) cross2(a[e], a[e + 1], b[e], b[e + 1], s);
+      }
+      int ca = seg * 2 + (odd ? 1 : 0), cb = seg * 2 + 1;   // the chunks that a and b hold
+      if (p.block > 64) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) b[e] = __shfl_xor_sync(0xffffffffu, b[e], R);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) cross2(a[e], a[e + 1], b[e], b[e + 1], s);
+        cb = odd ? seg * 2 - 1 : seg * 2 + 2;
+        for (int m = 2; m * 64 < p.block; m <<= 1) {
+          const float sg = seg & m ? -1.f : 1.f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float o0 = __shfl_xor_sync(0xffffffffu, a[e], m << lr), o1 = __shfl_xor_sync(0xffffffffu, a[e + 1], m << lr);
+            sfma2(a[e], a[e + 1], sg, o0, o1);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float o0 = __shfl_xor_sync(0xffffffffu, b[e], m << lr), o1 = __shfl_xor_sync(0xffffffffu, b[e + 1], m << lr);
+            sfma2(b[e], b[e + 1], sg, o0, o1);
+          }
+        }
+      }
+      uint4 pa, pb;
+      const uint32_t sa = quantize32(a, p.isb, pa), sb = quantize32(b, p.isb, pb);
+      // the four scale bytes of 128 columns meet in the even segment's lane
+      const uint32_t w = sa << (8 * (ca & 3)) | sb << (8 * (cb & 3));
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, w, R);
+      if (live) {
+        uint8_t* dst = p.codes + (size_t)(r0 + rl) * (K / 2);
+        *reinterpret_cast<uint4*>(dst + ca * 16) = pa;
+        *reinterpret_cast<uint4*>(dst + cb * 16) = pb;
+        if (!(seg & 1)) {
+          uint8_t* sf = p.sf + mx_sf_offset(r0 + rl, seg * 2, K);
+          if (seg + 1 < nseg) *reinterpret_cast<uint32_t*>(sf) = w | o;
+          else *reinterpret_cast<uint16_t*>(sf) = (uint16_t)w;   // K an odd multiple of 64
+        }
+      }
+    }
+    __syncthreads();   // everyone has read this group's rows
+    if (*abort_flag) {
+      // let the copies in flight land (bounded) before the shared memory goes away
+      if (threadIdx.x == 0) {
+        mbar_drain(&full[buf], (it >> 1) & 1, p.wait_ns);
+        if (g + (int)gridDim.x < p.ngroups) mbar_drain(&full[buf ^ 1], ((it + 1) >> 1) & 1, p.wait_ns);
+      }
+      break;
+    }
+    if (threadIdx.x == 0 && g + 2 * (int)gridDim.x < p.ngroups) {
+      fence_proxy_async_smem();
+      issue(g + 2 * gridDim.x, buf);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- dequantize
+// A thread per 8 codes: a 4-byte read, a scale byte, 8 values out; 2^tx threads
+// along a row.
 template <typename T>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes, const uint8_t* bscale, T* out,
-                                                            int rows, int K) {
+                                                            int rows, int K, int tx) {
   const int words = K / 8;
-  const int64_t n = (int64_t)rows * words;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int m = (int)(i / words), w = (int)(i % words);
-    const uint32_t c = reinterpret_cast<const uint32_t*>(codes)[i];
-    const float s = mx_scale(bscale[mx_sf_offset(m, w / 4, K)]);
+  const int x = threadIdx.x & ((1 << tx) - 1), y = threadIdx.x >> tx, per = 256 >> tx;
+  for (int m = (int)blockIdx.x * per + y; m < rows; m += (int)gridDim.x * per) {
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(codes) + (size_t)m * words;
+    T* o = out + (size_t)m * K;
+#pragma unroll 4
+    for (int w = x; w < words; w += 1 << tx) {
+      const uint32_t q = __ldg(c + w);
+      const float s = mx_scale(__ldg(bscale + mx_sf_offset(m, w / 4, K)));
+      float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) out[i * 8 + e] = (T)(e2m1_value((c >> (4 * e)) & 15u) * s);
+      for (int e = 0; e < 8; e += 2) {
+        uint32_t h;   // two E2M1 -> two FP16, exact
+        asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(q >> (4 * e)));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        v[e] = f.x * s;
+        v[e + 1] = f.y * s;
+      }
+      if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<float4*>(o)[2 * w] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(o)[2 * w + 1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        __nv_bfloat162 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        reinterpret_cast<uint4*>(o)[w] = *reinterpret_cast<const uint4*>(h);
+      }
+    }
   }
 }
 
 }  // namespace
 
+cudaError_t launch_mx_quantize(const K1Launch& a, cudaStream_t st) {
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void*>(mx_quantize_kernel));
+  if (e != cudaSuccess) return e;
+  const int sms = a.num_sms > 0 ? a.num_sms : 148;
+  auto bytes = [&](int lr) { return a.K / 64 * MXQ_SEG + (2 << lr) * (2 * a.K + (lr ? 128 >> lr : 0)) + 64; };
+  // rows per group: as many as put their gathers on different banks (8 rows: 2.1
+  // expected cycles for 32 lanes, 4 rows: 2.6, one row: 3.5) while two CTAs share
+  // an SM, or else one; a Hadamard block has to lie in one warp (32 / R segments
+  // of 64), and few rows are spread over the SMs
+  int lr = a.block <= 256 ? 3 : a.block == 512 ? 2 : 1;
+  while (lr > 0 && (a.rows >> lr) < sms) --lr;
+  if (bytes(lr) > 115000) {
+    int two = lr;
+    while (two > 1 && bytes(two) > 115000) --two;
+    if (two >= 2) lr = two;
+    else while (lr > 0 && bytes(lr) > 232000) --lr;
+  }
+  MxqParams p{};
+  p.x = a.x; p.rot = a.rot; p.codes = a.codes; p.sf = a.bscale;
+  p.status = a.status; p.wait_ns = a.wait_ns; p.inject_tx = a.inject_tx;
+  p.rows = a.rows; p.K = a.K; p.block = a.block; p.lr = lr; p.isb = a.inv_sqrt_b;
+  p.ngroups = (a.rows + (1 << lr) - 1) >> lr;
+  const int units = (a.K / 64 + (32 >> lr) - 1) / (32 >> lr);
+  const bool two = bytes(lr) <= 115000;
+  const int most = two ? 8 : 16, turns = (units + most - 1) / most;
+  const int warps = (units + turns - 1) / turns;   // an even share of a group's units each
+  const int grid = p.ngroups < sms * (two ? 2 : 1) ? p.ngroups : sms * (two ? 2 : 1);
+  mx_quantize_kernel<<<grid, warps * 32, bytes(lr), st>>>(p);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_mx_dequantize(const MxDequantLaunch& a, cudaStream_t st) {
-  const int64_t n = (int64_t)a.rows * (a.K / 8);
-  const int64_t blocks = (n + 255) / 256, most = (int64_t)(a.num_sms > 0 ? a.num_sms : 148) * 16;
+  int tx = 3;   // the threads along a row: a power of two up to 256, near a quarter of its words
+  while (tx < 8 && (4 << tx) < a.K / 8) ++tx;
+  const int per = 256 >> tx;
+  const int64_t blocks = ((int64_t)a.rows + per - 1) / per, most = (int64_t)(a.num_sms > 0 ? a.num_sms : 148) * 32;
   const int grid = (int)(blocks < most ? blocks : most);
   if (a.out_fp32)
-    mx_dequantize_kernel<float><<<grid, 256, 0, st>>>(a.codes, a.bscale, static_cast<float*>(a.out), a.rows, a.K);
+    mx_dequantize_kernel<float><<<grid, 256, 0, st>>>(a.codes, a.bscale, static_cast<float*>(a.out), a.rows, a.K, tx);
   else
-    mx_dequantize_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a.codes, a.bscale, static_cast<__nv_bfloat16*>(a.out), a.rows, a.K);
+    mx_dequantize_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a.codes, a.bscale, static_cast<__nv_bfloat16*>(a.out), a.rows, a.K, tx);
   return cudaGetLastError();
 }
 

@@ -26,7 +26,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -424,23 +423,12 @@ bool code_map(CUtensorMap* m, const uint8_t* codes, uint64_t rows, uint64_t cols
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The dynamic shared memory limit is raised once per kernel and device.
-template <class Kern>
-cudaError_t allow_smem(Kern k, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (done.load() >> (dev & 63) & 1u)) return e;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
-  return e;
-}
-
 // `tiles` x `ny` clusters, `steps` K steps to split.
 template <int MODE>
 cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int steps, int sms, cudaStream_t st) {
   constexpr int NA = MODE == GATE_UP ? 2 : 1;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(mx_few_kernel<MODE>, done);
+  static SmemLimit limit_once;
+  cudaError_t e = limit_once.raise(reinterpret_cast<const void*>(mx_few_kernel<MODE>));
   if (e != cudaSuccess) return e;
   // ranks per cluster: the fewest that give every SM a CTA, two steps each at least
   int S = 1;
