@@ -1,5 +1,6 @@
 // Internal launch descriptors shared by the C-ABI layer and the kernels.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -134,6 +135,12 @@ struct MoeLaunch {
   uint64_t wait_ns;
   uint32_t inject_tx;
 };
+// Tensor maps: packed codes, rows x cols / 2 bytes in boxes of 128 bytes x
+// box_rows; BF16 output in 32 x 32 boxes (64-byte swizzle, cols % 8 == 0)
+bool mx_code_map(CUtensorMap* m, const uint8_t* codes, uint64_t rows, uint64_t cols, uint32_t box_rows);
+bool mx_out_map(CUtensorMap* m, void* Y, uint64_t rows, uint64_t cols);
+// MXFP4 products of more tokens, without the low-rank branch (rq_mxgemm.cu)
+cudaError_t launch_mx_gemm(const GemmLaunch& a, cudaStream_t st, const char** why);
 // MXFP4 products of at most MX_FEW_TOKENS tokens (rq_mxfew.cu)
 constexpr int MX_FEW_TOKENS = 64;
 cudaError_t launch_mx_few(const GemmLaunch& a, cudaStream_t st, const char** why);

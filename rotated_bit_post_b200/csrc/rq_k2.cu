@@ -1530,6 +1530,7 @@ cudaError_t launch_pair(Kern k, int smem, int pairs, int threads, const TMaps& t
 
 cudaError_t launch_gemm(const GemmLaunch& a, cudaStream_t st, const char** why) {
   if (a.a_fmt == RQ_FMT_MXFP4 && a.M <= MX_FEW_TOKENS) return launch_mx_few(a, st, why);
+  if (a.a_fmt == RQ_FMT_MXFP4 && !a.c) return launch_mx_gemm(a, st, why);
   TMaps tm;
   memset(&tm, 0, sizeof(tm));
   GemmParams gp{};
@@ -1567,10 +1568,8 @@ cudaError_t launch_gemm(const GemmLaunch& a, cudaStream_t st, const char** why) 
     ok &= make_map_2d(&tm.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, a.K / 2, a.N, a.K / 2, 128, BN,
                       CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) { *why = "cuTensorMapEncodeTiled failed"; return cudaErrorInvalidValue; }
-    if (mxf4) {
-      if (BN == 256) return launch(gemm_nvf4_kernel<256, true>, Nvf4Plan<256, true>::BYTES, grid, NVF4_THREADS, tm, gp, st);
+    if (mxf4)   // (with the low-rank branch; without it MXFP4 runs in rq_mxgemm.cu)
       return launch(gemm_nvf4_kernel<128, true>, Nvf4Plan<128, true>::BYTES, grid, NVF4_THREADS, tm, gp, st);
-    }
     if (BN == 256) return launch(gemm_nvf4_kernel<256, false>, Nvf4Plan<256, false>::BYTES, grid, NVF4_THREADS, tm, gp, st);
     return launch(gemm_nvf4_kernel<128, false>, Nvf4Plan<128, false>::BYTES, grid, NVF4_THREADS, tm, gp, st);
   }

@@ -4,6 +4,7 @@
 // MXFP4 has no row scale: a block of 32 rotated coordinates is quantized from
 // its own maximum, so one pass over the transformed values in registers is
 // all there is, and no thread waits for a row's other blocks.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -303,7 +304,38 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes
   }
 }
 
+// ------------------------------------------------------------------ tensor maps
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn find_encode() {
+  void* f = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess)
+    return reinterpret_cast<EncodeTiledFn>(f);
+  return nullptr;
+}
+
+bool map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows, uint64_t pitch,
+            uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  static const EncodeTiledFn enc = find_encode();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {inner, rows}, strides[1] = {pitch};
+  cuuint32_t box[2] = {box_inner, box_rows}, es[2] = {1, 1};
+  return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
+
+bool mx_code_map(CUtensorMap* m, const uint8_t* codes, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  return map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, cols / 2, rows, cols / 2, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool mx_out_map(CUtensorMap* m, void* Y, uint64_t rows, uint64_t cols) {
+  return map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, cols, rows, cols * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
 
 cudaError_t launch_mx_quantize(const K1Launch& a, cudaStream_t st) {
   static SmemLimit limit;

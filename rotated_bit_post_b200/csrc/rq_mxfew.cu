@@ -399,30 +399,6 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn find_encode() {
-  void* f = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-      q == cudaDriverEntryPointSuccess)
-    return reinterpret_cast<EncodeTiledFn>(f);
-  return nullptr;
-}
-
-// rows x cols/2 bytes of packed codes in boxes of 128 bytes x `box` rows
-bool code_map(CUtensorMap* m, const uint8_t* codes, uint64_t rows, uint64_t cols, uint32_t box) {
-  static const EncodeTiledFn enc = find_encode();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {cols / 2, rows}, strides[1] = {cols / 2};
-  cuuint32_t b[2] = {128, box}, es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, b, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // `tiles` x `ny` clusters, `steps` K steps to split.
 template <int MODE>
 cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int steps, int sms, cudaStream_t st) {
@@ -481,7 +457,7 @@ cudaError_t launch_mx_few(const GemmLaunch& a, cudaStream_t st, const char** why
   p.c = a.c; p.L = a.L; p.r = a.r;
   p.Y = a.Y; p.out_fp32 = a.out_fp32;
   p.status = a.status; p.wait_ns = a.wait_ns; p.inject_tx = a.inject_tx;
-  if (!code_map(&tm.w, a.w_codes, a.N, a.K, 128) || !code_map(&tm.x, a.a_codes, a.M, a.K, p.NT)) {
+  if (!mx_code_map(&tm.w, a.w_codes, a.N, a.K, 128) || !mx_code_map(&tm.x, a.a_codes, a.M, a.K, p.NT)) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
@@ -499,7 +475,7 @@ cudaError_t launch_moe_products(const MoeLaunch& a, const uint8_t* xq, const uin
   p.idx = a.idx; p.wts = a.wts; p.top_k = a.top_k;
   p.hq = hq; p.hq_sf = hq_sf; p.block2 = a.block2; p.inv_sqrt_b2 = a.inv_sqrt_b2;
   p.status = a.status; p.wait_ns = a.wait_ns; p.inject_tx = a.inject_tx;
-  if (!code_map(&tm.w, a.w1, (uint64_t)a.E * 2 * a.I, a.K, 128) || !code_map(&tm.x, xq, a.T, a.K, p.NT))
+  if (!mx_code_map(&tm.w, a.w1, (uint64_t)a.E * 2 * a.I, a.K, 128) || !mx_code_map(&tm.x, xq, a.T, a.K, p.NT))
     return cudaErrorInvalidValue;
   cudaError_t e = launch_mode<GATE_UP>(tm, p, a.I / 128, active, (a.K + 255) / 256, sms, st);
   if (e != cudaSuccess) return e;
@@ -508,8 +484,8 @@ cudaError_t launch_moe_products(const MoeLaunch& a, const uint8_t* xq, const uin
   p.w_sf = a.w2_sf; p.w_sf_expert = mx_sf_bytes(a.K, a.I);
   p.x_sf = hq_sf;
   p.Y = a.Y; p.out_fp32 = a.out_fp32;
-  if (!code_map(&tm.w, a.w2, (uint64_t)a.E * a.K, a.I, 128) ||
-      !code_map(&tm.x, hq, (uint64_t)active * a.T, a.I, p.NT))
+  if (!mx_code_map(&tm.w, a.w2, (uint64_t)a.E * a.K, a.I, 128) ||
+      !mx_code_map(&tm.x, hq, (uint64_t)active * a.T, a.I, p.NT))
     return cudaErrorInvalidValue;
   return launch_mode<DOWN>(tm, p, (a.K + 127) / 128, 1, active * ((a.I + 255) / 256), sms, st);
 }

@@ -325,7 +325,8 @@ def test_dequantize(L, rows, K):
 # ------------------------------------------------------------------ GPU: product
 SHAPES = [(1, 1, 64), (1, 128, 192), (2, 300, 4096), (7, 129, 1152), (8, 256, 320), (16, 1000, 2048), (17, 4100, 512),
           (33, 64, 1344), (64, 640, 1152), (65, 384, 1024), (128, 256, 256), (130, 1153, 320), (257, 515, 1152),
-          (1, 77, 16384), (300, 260, 4160)]
+          (1, 77, 16384), (300, 260, 4160),
+          (2600, 2104, 192), (2600, 2101, 448), (5000, 1280, 1152)]
 
 
 @pytest.mark.gpu
