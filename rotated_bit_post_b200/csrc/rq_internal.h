@@ -136,8 +136,9 @@ struct MoeLaunch {
   uint32_t inject_tx;
 };
 // Tensor maps: packed codes, rows x cols / 2 bytes in boxes of 128 bytes x
-// box_rows; BF16 output in 32 x 32 boxes (64-byte swizzle, cols % 8 == 0)
+// box_rows; scale tiles, 512 bytes a row, in pairs; BF16 output in 32 x 32 boxes (64-byte swizzle, cols % 8 == 0)
 bool mx_code_map(CUtensorMap* m, const uint8_t* codes, uint64_t rows, uint64_t cols, uint32_t box_rows);
+bool mx_scale_map(CUtensorMap* m, const uint8_t* sf, uint64_t rows, uint64_t cols);
 bool mx_out_map(CUtensorMap* m, void* Y, uint64_t rows, uint64_t cols);
 // MXFP4 products of more tokens, without the low-rank branch (rq_mxgemm.cu)
 cudaError_t launch_mx_gemm(const GemmLaunch& a, cudaStream_t st, const char** why);

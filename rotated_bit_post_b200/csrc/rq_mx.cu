@@ -333,6 +333,10 @@ bool map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t
 bool mx_code_map(CUtensorMap* m, const uint8_t* codes, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   return map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, cols / 2, rows, cols / 2, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
+bool mx_scale_map(CUtensorMap* m, const uint8_t* sf, uint64_t rows, uint64_t cols) {
+  return map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, sf, 128, (rows + 127) / 128 * ((cols + 127) / 128), 512, 128, 2,
+                CU_TENSOR_MAP_SWIZZLE_NONE);
+}
 bool mx_out_map(CUtensorMap* m, void* Y, uint64_t rows, uint64_t cols) {
   return map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, cols, rows, cols * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }

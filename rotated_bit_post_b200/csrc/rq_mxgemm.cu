@@ -5,10 +5,10 @@
 // 256-wide K step, 35 KB for 512 cycles of MMA.  A single CTA's 128 x 256 tile
 // needs 51 KB for as many, more than an SM takes from L2 in that time.
 //
-// Per CTA: warp 0 issues the copies; warp 1 the pair's MMAs (even CTA) or passes
-// the odd CTA's landed stages on; warp 2 moves the scales to TMEM on an issue
-// stream of its own (even CTA, both CTAs' tiles at once), a ring of slots ahead of
-// the MMAs; warps 4-11 are the epilogue.  The accumulator takes 256 of the
+// Per CTA: warp 0 issues the copies, warps 12-15 write the landed scales to
+// TMEM (tcgen05.st: as tcgen05.cp they would take 25 ns each of the tensor pipe, 150
+// of the 270 ns that a step's MMAs run) and report the stage to the even CTA,
+// whose warp 1 issues the pair's MMAs; warps 4-11 are the epilogue.  The accumulator takes 256 of the
 // 512 TMEM columns and is single: the epilogue brings it into registers as
 // packed BF16 first, hands it back, and stores while the next tile runs.
 #include <cuda.h>
@@ -26,25 +26,25 @@ namespace rq {
 
 namespace {
 
-constexpr int MG_THREADS = 384;
-constexpr int MG_STAGES = 5;
-constexpr int MG_SLOTS = 4;              // scale slots in TMEM
-constexpr int MG_SLOT_COLS = 24;         // 2 scale tiles of 4 columns for A, 4 for B
+constexpr int MG_THREADS = 512;
+constexpr int MG_STAGES = 6;
+constexpr int MG_SLOT_COLS = 24;         // TMEM columns of a stage's scales: 2 tiles of 4 for A, 4 for B
 constexpr int MG_PA = 128 * 128, MG_PB = 128 * 128, MG_SA = 1024, MG_SB = 2048;
 constexpr int MG_STAGE = MG_PA + MG_PB + MG_SA + MG_SB;
-constexpr int MG_STG = 4096;             // an epilogue warp's two 32 x 32 BF16 boxes
+constexpr int MG_STG = 2048;             // an epilogue warp's 32 x 32 BF16 box
 constexpr int MG_OFF_STG = MG_STAGES * MG_STAGE;
 constexpr int MG_OFF_BAR = MG_OFF_STG + 8 * MG_STG;
-constexpr int MG_BYTES = MG_OFF_BAR + 512 + 1024;
+constexpr int MG_BYTES = MG_OFF_BAR + 512;   // (no slack: the base has to be 1024-byte aligned)
 static_assert(MG_BYTES <= 232448, "shared memory plan exceeds 227 KB");
 
 struct __align__(64) MgMaps {
-  CUtensorMap a, b, y;
+  CUtensorMap a, b;     // packed codes
+  CUtensorMap sa, sb;   // scale tiles, 512 bytes a row
+  CUtensorMap y;
 };
 
 struct MgParams {
   int M, N, K;
-  const uint8_t *a_sf, *w_sf;
   void* Y;
   int out_fp32, tma_store;
   int32_t* status;
@@ -57,21 +57,28 @@ __device__ __forceinline__ uint32_t mg_idesc(uint32_t id) {
   return (id << 4) | (1u << 7) | (1u << 10) | (32u << 17) | (1u << 23) | (16u << 24) | (id << 29);
 }
 
+// 8 consecutive TMEM columns of the warp's 32 lanes
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const uint4& b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_constant__ MgMaps tm,
                                                                 const __grid_constant__ MgParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {   // (both CTAs see the same base)
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, ST_SMEM_ALIGN);
+    return;
+  }
   const uint32_t sbase = smem_u32(smem);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + MG_OFF_BAR);   // this CTA's copies landed
-  uint64_t* pfull = full + MG_STAGES;      // even CTA: the odd CTA's copies landed
-  uint64_t* empty = pfull + MG_STAGES;     // the pair's MMAs have read the stage
-  uint64_t* sffull = empty + MG_STAGES;    // even CTA: scales in TMEM
-  uint64_t* sfempty = sffull + MG_SLOTS;   // even CTA: MMAs done with a slot
-  uint64_t* accfull = sfempty + MG_SLOTS;
+  uint64_t* ready = full + MG_STAGES;      // even CTA: landed and scales in TMEM, in both CTAs
+  uint64_t* empty = ready + MG_STAGES;     // the pair's MMAs have read the stage
+  uint64_t* accfull = empty + MG_STAGES;
   uint64_t* accempty = accfull + 1;        // even CTA: both CTAs' epilogue warps have read the accumulator
   uint64_t* mdrain = accempty + 1;
-  uint64_t* cdrain = mdrain + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cdrain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -81,16 +88,16 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
   const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < MG_STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&pfull[i], 1); mbar_init(&empty[i], 1); }
-    for (int i = 0; i < MG_SLOTS; ++i) { mbar_init(&sffull[i], 1); mbar_init(&sfempty[i], 1); }
+    for (int i = 0; i < MG_STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&ready[i], 8); mbar_init(&empty[i], 1); }
     mbar_init(accfull, 1);
     mbar_init(accempty, 16);
     mbar_init(mdrain, 1);
-    mbar_init(cdrain, 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm.a);
     prefetch_tmap(&tm.b);
+    prefetch_tmap(&tm.sa);
+    prefetch_tmap(&tm.sb);
   }
   if (warp == 1) {
     tmem_alloc2(tmem_slot, 512);
@@ -108,9 +115,6 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
       bool ok = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
         const int m0 = tile / nN * 256 + (int)rank * 128, n0 = tile % nN * 256;
-        // scale tiles exist for row tiles that hold a row
-        const bool has_a = m0 < p.M;
-        const int nb = min(2, (p.N + 127) / 128 - n0 / 128);
         for (int kt = 0; kt < nk; ++kt, ++kc) {
           const int s = kc % MG_STAGES;
           ok = (kc < (uint32_t)MG_STAGES ||
@@ -118,51 +122,41 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
                !*abort_flag;
           if (!ok) break;
           uint8_t* st = smem + s * MG_STAGE;
-          const uint32_t sfb = (uint32_t)min(2, KT - kt * 2) * 512;   // scale bytes of 128 rows
-          mbar_expect_tx(&full[s], MG_PA + MG_PB + (nb + (has_a ? 1 : 0)) * sfb + (kc == 0 ? p.inject_tx : 0u));
-          tma_load_2d(st, &tm.a, kt * 128, m0, &full[s]);
-          tma_load_2d(st + MG_PA, &tm.b, kt * 128, n0 + (int)rank * 128, &full[s]);
-          if (has_a) bulk_g2s(st + MG_PA + MG_PB, p.a_sf + ((size_t)(m0 / 128) * KT + kt * 2) * 512, sfb, &full[s]);
-          for (int b = 0; b < nb; ++b)   // every CTA of the pair multiplies all 256 weight rows
-            bulk_g2s(st + MG_PA + MG_PB + MG_SA + b * 1024, p.w_sf + ((size_t)(n0 / 128 + b) * KT + kt * 2) * 512, sfb, &full[s]);
+          mbar_expect_tx(&full[s], MG_STAGE + (kc == 0 ? p.inject_tx : 0u));
+          uint64_t* bar = &full[s];
+          tma_load_2d(st, &tm.a, kt * 128, m0, bar);
+          tma_load_2d(st + MG_PA, &tm.b, kt * 128, n0 + (int)rank * 128, bar);
+          // two scale tiles per 128 rows (past the end: the next rows', or zeros, not used)
+          tma_load_2d(st + MG_PA + MG_PB, &tm.sa, 0, m0 / 128 * KT + kt * 2, bar);
+#pragma unroll
+          for (int b = 0; b < 2; ++b)   // each CTA multiplies all 256 weight rows
+            tma_load_2d(st + MG_PA + MG_PB + MG_SA + b * 1024, &tm.sb, 0, (n0 / 128 + b) * KT + kt * 2, bar);
         }
       }
-      if (ok)   // the last commits land in this CTA's barriers: it may not leave before
-        for (uint32_t c = kc > (uint32_t)MG_STAGES ? kc - MG_STAGES : 0; c < kc && ok; ++c)
-          ok = mbar_wait(&empty[c % MG_STAGES], (c / MG_STAGES) & 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns);
+      // the last commits arrive in this CTA's barriers: it may not leave before
+      const uint32_t c0 = kc > (uint32_t)MG_STAGES ? kc - MG_STAGES : 0;
+      for (uint32_t c = c0; c < kc && ok; ++c)
+        ok = mbar_wait(&empty[c % MG_STAGES], (c / MG_STAGES) & 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns);
       if (!ok)   // let the copies already issued land (bounded)
-        for (uint32_t c = kc > (uint32_t)MG_STAGES ? kc - MG_STAGES : 0; c < kc; ++c)
-          mbar_drain(&full[c % MG_STAGES], (c / MG_STAGES) & 1, p.wait_ns);
-    }
-  } else if (warp == 1 && rank == 1) {
-    // ------------------------------------------------------------ the odd CTA's stages, passed on
-    if (lane == 0) {
-      uint32_t kc = 0;
-      bool ok = true;
-      for (int tile = tile0; tile < ntiles && ok; tile += tstep)
-        for (int kt = 0; kt < nk && ok; ++kt, ++kc) {
-          const int s = kc % MG_STAGES;
-          ok = mbar_wait(&full[s], (kc / MG_STAGES) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
-          if (ok) mbar_arrive_cluster(&pfull[s], 0);
-        }
+        for (uint32_t c = c0; c < kc; ++c) mbar_drain(&full[c % MG_STAGES], (c / MG_STAGES) & 1, p.wait_ns);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       uint32_t kc = 0;
       int tc = 0;
       bool ok = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++tc) {
-        ok = tc == 0 || mbar_wait(accempty, (tc - 1) & 1, p.status, ST_TIMEOUT_EPI, abort_flag, p.wait_ns);
-        if (!ok) break;
-        tc_fence_after();
         for (int kt = 0; kt < nk; ++kt, ++kc) {
-          const int s = kc % MG_STAGES, sl = kc % MG_SLOTS;
-          ok = mbar_wait(&full[s], (kc / MG_STAGES) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns) &&
-               mbar_wait(&pfull[s], (kc / MG_STAGES) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns) &&
-               mbar_wait(&sffull[sl], (kc / MG_SLOTS) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+          const int s = kc % MG_STAGES;
+          ok = mbar_wait(&ready[s], (kc / MG_STAGES) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = sbase + s * MG_STAGE, tsf = tmem + 256 + sl * MG_SLOT_COLS;
+          const uint32_t st = sbase + s * MG_STAGE, tsf = tmem + 256 + s * MG_SLOT_COLS;
+          if (kt == 0 && tc > 0) {
+            ok = mbar_wait(accempty, (tc - 1) & 1, p.status, ST_TIMEOUT_EPI, abort_flag, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+          }
           const int kkn = min(4, p.K / 64 - kt * 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -170,7 +164,6 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
               umma_mxf4_2(tmem, smem_desc(st + kk * 32, 16, 1024, 2), smem_desc(st + MG_PA + kk * 32, 16, 1024, 2),
                           mg_idesc((kk & 1) * 2), tsf + (kk >> 1) * 4, tsf + 8 + (kk >> 1) * 8, kt > 0 || kk > 0);
           tc_commit2_mc(&empty[s], 0x3);
-          tc_commit2_mc(&sfempty[sl], 0x1);
         }
         if (ok) tc_commit2_mc(accfull, 0x3);
       }
@@ -179,35 +172,32 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
         mbar_drain(mdrain, 0, p.wait_ns);
       }
     }
-  } else if (warp == 2 && rank == 0) {
-    // ------------------------------------------------------------ scales -> TMEM, in both CTAs
-    if (lane == 0) {
-      uint32_t kc = 0;
-      bool ok = true;
-      for (int tile = tile0; tile < ntiles && ok; tile += tstep)
-        for (int kt = 0; kt < nk; ++kt, ++kc) {
-          const int s = kc % MG_STAGES, sl = kc % MG_SLOTS;
-          ok = (kc < (uint32_t)MG_SLOTS ||
-                mbar_wait(&sfempty[sl], (kc / MG_SLOTS - 1) & 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns)) &&
-               mbar_wait(&full[s], (kc / MG_STAGES) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns) &&
-               mbar_wait(&pfull[s], (kc / MG_STAGES) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sf = sbase + s * MG_STAGE + MG_PA + MG_PB, tsf = tmem + 256 + sl * MG_SLOT_COLS;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {   // 128 columns each; B: 8 TMEM columns of 256 rows
-            tc_cp2_32x128b_warpx4(tsf + q * 4, smem_desc(sf + q * 512, 16, 128, 0));
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-              tc_cp2_32x128b_warpx4(tsf + 8 + q * 8 + b * 4, smem_desc(sf + MG_SA + b * 1024 + q * 512, 16, 128, 0));
-          }
-          tc_commit2_mc(&sffull[sl], 0x1);
-        }
-      if (!ok) {
-        tc_commit2_mc(cdrain, 0x1);
-        mbar_drain(cdrain, 0, p.wait_ns);
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ scales -> TMEM
+    // one warp per lane quadrant: every quadrant holds the same 32 rows x 24
+    // columns, word (l, c) of a tile the scale bytes of row 32 c + l
+    const uint32_t quad = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256;
+    uint32_t kc = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < ntiles && ok; tile += tstep)
+      for (int kt = 0; kt < nk; ++kt, ++kc) {
+        const int s = kc % MG_STAGES;
+        ok = mbar_wait(&full[s], (kc / MG_STAGES) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+        if (!ok) break;
+        tc_fence_after();   // (the stage's columns are free: its MMAs were done before it was filled again)
+        const uint4* sf = reinterpret_cast<const uint4*>(smem + s * MG_STAGE + MG_PA + MG_PB) + lane;
+        uint4 w[6];   // A: 2 x 128 columns; B: 2 x 128 columns of two row tiles
+        w[0] = sf[0]; w[1] = sf[32];
+        w[2] = sf[64]; w[3] = sf[128];
+        w[4] = sf[96]; w[5] = sf[160];
+        tmem_st8(quad + s * MG_SLOT_COLS, w[0], w[1]);
+        tmem_st8(quad + s * MG_SLOT_COLS + 8, w[2], w[3]);
+        tmem_st8(quad + s * MG_SLOT_COLS + 16, w[4], w[5]);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(&ready[s], 0);
       }
-    }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
@@ -264,9 +254,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
       if (p.tma_store) {
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
-          // two boxes in turn: the store two back has read this one
-          const uint32_t buf = stg + (ch & 1) * 2048;
-          if (lane == 0) bulk_wait_group_read<1>();
+          const uint32_t buf = stg;
+          if (lane == 0) bulk_wait_group_read<0>();   // the last store has read the box
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -312,11 +301,11 @@ cudaError_t launch_mx_gemm(const GemmLaunch& a, cudaStream_t st, const char** wh
   MgMaps tm;
   MgParams p{};
   p.M = a.M; p.N = a.N; p.K = a.K;
-  p.a_sf = a.a_bscale; p.w_sf = a.w_bscale;
   p.Y = a.Y; p.out_fp32 = a.out_fp32;
   p.tma_store = !a.out_fp32 && a.N % 8 == 0;   // (the map's row pitch must be a multiple of 16 bytes)
   p.status = a.status; p.wait_ns = a.wait_ns; p.inject_tx = a.inject_tx;
-  bool ok = mx_code_map(&tm.a, a.a_codes, a.M, a.K, 128) && mx_code_map(&tm.b, a.w_codes, a.N, a.K, 128);
+  bool ok = mx_code_map(&tm.a, a.a_codes, a.M, a.K, 128) && mx_code_map(&tm.b, a.w_codes, a.N, a.K, 128) &&
+            mx_scale_map(&tm.sa, a.a_bscale, a.M, a.K) && mx_scale_map(&tm.sb, a.w_bscale, a.N, a.K);
   if (p.tma_store) ok = ok && mx_out_map(&tm.y, a.Y, a.M, a.N);
   if (!ok) {
     *why = "cuTensorMapEncodeTiled failed";
