@@ -84,7 +84,13 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // when another thread has already flagged an abort in *abort_flag.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_t* status, int32_t code,
                                           volatile int32_t* abort_flag, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+  // The clock is read only after a long row of attempts (each may suspend the
+  // thread for up to the hint's 1 ms): reading it takes about half a
+  // microsecond, which a wait that ends meanwhile would pay in full.
+  for (int i = 0; i < 64; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (abort_flag && *abort_flag) return false;
+  }
   const uint64_t t0 = globaltimer();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
