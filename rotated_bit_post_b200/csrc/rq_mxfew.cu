@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
   uint16_t* act = reinterpret_cast<uint16_t*>(bits + 8);
   float* part = reinterpret_cast<float*>(smem);       // [NA][NT][FEW_PITCH], over the stages once they are used up
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   uint32_t S;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
@@ -191,78 +191,92 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
   const int n = live ? (int)((int64_t)total * (rank + 1) / S) - s0 : 0;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const size_t rowt = (size_t)(n0 / 128) * KT * 512;   // this row tile's scales
-      auto load = [&](int i, bool wt, bool tk) {
-        const int st = s0 + i, a = MODE == DOWN ? st / spe : 0, kt = MODE == DOWN ? st - a * spe : st;
-        const int e = MODE == DOWN ? act[a] : expert;
-        uint64_t* bar = &full[i % p.stages];
-        uint8_t* s = smem + (i % p.stages) * STAGE;
-        const uint32_t sfb = (uint32_t)min(2, KT - kt * 2) * 512;   // scale bytes of 128 rows
-        if (wt) {
-          mbar_expect_tx(bar, NA * (PA + sfb) + PB + sfb + (i == 0 ? p.inject_tx : 0u));
-          const uint8_t* sf = p.w_sf + (MODE == LINEAR ? 0 : (size_t)e * p.w_sf_expert) + (size_t)kt * 1024;
+    const bool one = elect_one();
+    const size_t rowt = (size_t)(n0 / 128) * KT * 512;   // this row tile's scales
+    // position of a step: stage and its phase, K step of the expert, place in
+    // the list of active experts (counted on: a division costs more than the rest)
+    struct Pos { int s, ph, kt, a; };
+    auto next = [&](Pos& q) {
+      if (++q.s == p.stages) { q.s = 0; q.ph ^= 1; }
+      if (++q.kt == spe) { q.kt = 0; ++q.a; }
+    };
+    auto load = [&](const Pos& q, bool first, bool wt, bool tk) {
+      const int e = MODE == DOWN ? __shfl_sync(0xffffffffu, (int)act[q.a], 0) : expert;
+      if (!one) return;
+      uint64_t* bar = &full[q.s];
+      uint8_t* s = smem + q.s * STAGE;
+      const uint32_t sfb = (uint32_t)min(2, KT - q.kt * 2) * 512;   // scale bytes of 128 rows
+      if (wt) {
+        mbar_expect_tx(bar, NA * (PA + sfb) + PB + sfb + (first ? p.inject_tx : 0u));
+        const uint8_t* sf = p.w_sf + (MODE == LINEAR ? 0 : (size_t)e * p.w_sf_expert) + (size_t)q.kt * 1024;
 #pragma unroll
-          for (int h = 0; h < NA; ++h) {   // GATE_UP: rows I..2I-1 are the up rows
-            const int row = (MODE == LINEAR ? 0 : e * NA * p.N) + h * p.N + n0;
-            tma_load_2d(s + h * PA, &tm.w, kt * 128, row, bar);
-            bulk_g2s(s + NA * PA + PB + h * SF, sf + (size_t)h * (p.N / 128) * KT * 512 + rowt, sfb, bar);
-          }
+        for (int h = 0; h < NA; ++h) {   // GATE_UP: rows I..2I-1 are the up rows
+          const int row = (MODE == LINEAR ? 0 : e * NA * p.N) + h * p.N + n0;
+          tma_load_2d(s + h * PA, &tm.w, q.kt * 128, row, bar);
+          bulk_g2s(s + NA * PA + PB + h * SF, sf + (size_t)h * (p.N / 128) * KT * 512 + rowt, sfb, bar);
         }
-        if (tk) {
-          tma_load_2d(s + NA * PA, &tm.x, kt * 128, a * p.T, bar);
-          bulk_g2s(s + NA * (PA + SF) + PB, p.x_sf + (size_t)a * KT * 512 + (size_t)kt * 1024, sfb, bar);
-        }
-      };
-      int i = 0;
-      if (p.early) {   // the first stages' weights now, their tokens once the previous kernel is done
-        const int head = min(n, p.stages);
-        for (int j = 0; j < head; ++j) load(j, true, false);
-        griddep_wait();
-        for (; i < head; ++i) load(i, false, true);
       }
-      for (; i < n; ++i) {
-        if (i >= p.stages &&
-            !mbar_wait(&empty[i % p.stages], ((i / p.stages) - 1) & 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns))
-          break;
-        load(i, true, true);
+      if (tk) {
+        const int a = MODE == DOWN ? q.a : 0;
+        tma_load_2d(s + NA * PA, &tm.x, q.kt * 128, a * p.T, bar);
+        bulk_g2s(s + NA * (PA + SF) + PB, p.x_sf + (size_t)a * KT * 512 + (size_t)q.kt * 1024, sfb, bar);
       }
-      if (*abort_flag)   // let the copies already issued land (bounded)
-        for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j) mbar_drain(&full[j % p.stages], (j / p.stages) & 1, p.wait_ns);
+    };
+    Pos q{0, 0, s0 % spe, s0 / spe};
+    int i = 0;
+    if (p.early) {   // the first stages' weights now, their tokens once the previous kernel is done
+      const int head = min(n, p.stages);
+      const Pos q0 = q;
+      for (int j = 0; j < head; ++j) { load(q, j == 0, true, false); next(q); }
+      griddep_wait();
+      q = q0;
+      for (; i < head; ++i) { load(q, false, false, true); next(q); }
     }
+    for (; i < n; ++i) {
+      if (i >= p.stages && !warp_wait(&empty[q.s], q.ph ^ 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns)) break;
+      load(q, i == 0, true, true);
+      next(q);
+    }
+    if (i < n)   // let the copies already issued land (bounded)
+      for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j) mbar_drain(&full[j % p.stages], (j / p.stages) & 1, p.wait_ns);
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
+      const bool one = elect_one();
       bool ok = true;
+      int s = 0, ph = 0, kt = s0 % spe;
       for (int i = 0; i < n; ++i) {
-        const int s = i % p.stages;
-        ok = mbar_wait(&full[s], (i / p.stages) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+        ok = warp_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
-        const int kt = MODE == DOWN ? (s0 + i) % spe : s0 + i;
         const int sct = min(2, KT - kt * 2), kkn = min(4, p.K / 64 - kt * 4);
         const uint32_t st = sbase + s * STAGE;
         // a slot of scale columns per stage: free again when the stage is
         const uint32_t tsf = tmem + NA * p.NT + s * (NA + 1) * 8;
-        for (int q = 0; q < sct; ++q) {
+        if (one) {
 #pragma unroll
-          for (int h = 0; h <= NA; ++h)   // weight scales, then the tokens'
-            tc_cp_32x128b_warpx4(tsf + h * 8 + q * 4, smem_desc(st + NA * PA + PB + h * SF + q * 512, 16, 128, 0));
+          for (int q = 0; q < 2; ++q)
+            if (q < sct) {
+#pragma unroll
+              for (int h = 0; h <= NA; ++h)   // weight scales, then the tokens'
+                tc_cp_32x128b_warpx4(tsf + h * 8 + q * 4, smem_desc(st + NA * PA + PB + h * SF + q * 512, 16, 128, 0));
+            }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (kk < kkn) {
+#pragma unroll
+              for (int h = 0; h < NA; ++h)
+                umma_mxf4(tmem + h * p.NT, smem_desc(st + h * PA + kk * 32, 16, 1024, 2),
+                          smem_desc(st + NA * PA + kk * 32, 16, 1024, 2), few_idesc(p.NT, (kk & 1) * 2),
+                          tsf + h * 8 + (kk >> 1) * 4, tsf + NA * 8 + (kk >> 1) * 4, i > 0 || kk > 0);
+            }
+          tc_commit(&empty[s]);
+          if (i == n - 1) tc_commit(accfull);
         }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (kk < kkn) {
-#pragma unroll
-            for (int h = 0; h < NA; ++h)
-              umma_mxf4(tmem + h * p.NT, smem_desc(st + h * PA + kk * 32, 16, 1024, 2),
-                        smem_desc(st + NA * PA + kk * 32, 16, 1024, 2), few_idesc(p.NT, (kk & 1) * 2),
-                        tsf + h * 8 + (kk >> 1) * 4, tsf + NA * 8 + (kk >> 1) * 4, i > 0 || kk > 0);
-          }
-        tc_commit(&empty[s]);
+        if (++s == p.stages) { s = 0; ph ^= 1; }
+        if (++kt == spe) kt = 0;
       }
-      if (ok) {
-        tc_commit(accfull);
-      } else {   // wait (bounded) for the MMAs already issued
-        tc_commit(mdrain);
+      if (!ok) {   // wait (bounded) for the MMAs already issued
+        if (one) tc_commit(mdrain);
         mbar_drain(mdrain, 0, p.wait_ns);
       }
     }

@@ -5,12 +5,11 @@
 // 256-wide K step, 35 KB for 512 cycles of MMA.  A single CTA's 128 x 256 tile
 // needs 51 KB for as many, more than an SM takes from L2 in that time.
 //
-// Per CTA: warp 0 issues the copies, warps 12-15 write the landed scales to
-// TMEM (tcgen05.st: as tcgen05.cp they would take 25 ns each of the tensor pipe, 150
-// of the 270 ns that a step's MMAs run) and report the stage to the even CTA,
-// whose warp 1 issues the pair's MMAs; warps 4-11 are the epilogue.  The accumulator takes 256 of the
-// 512 TMEM columns and is single: the epilogue brings it into registers as
-// packed BF16 first, hands it back, and stores while the next tile runs.
+// Per CTA: warp 0 issues the copies, which count on the even CTA's barrier; warp
+// 1 (even CTA) copies both CTAs' scales to TMEM and issues the pair's MMAs; warps
+// 4-11 are the epilogue.  The accumulator takes 256 of the 512 TMEM columns and
+// is single: the epilogue brings it into registers as packed BF16 first, hands
+// it back, and stores while the next tile runs.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -26,7 +25,7 @@ namespace rq {
 
 namespace {
 
-constexpr int MG_THREADS = 512;
+constexpr int MG_THREADS = 384;
 constexpr int MG_STAGES = 6;
 constexpr int MG_SLOT_COLS = 24;         // TMEM columns of a stage's scales: 2 tiles of 4 for A, 4 for B
 constexpr int MG_PA = 128 * 128, MG_PB = 128 * 128, MG_SA = 1024, MG_SB = 2048;
@@ -57,13 +56,6 @@ __device__ __forceinline__ uint32_t mg_idesc(uint32_t id) {
   return (id << 4) | (1u << 7) | (1u << 10) | (32u << 17) | (1u << 23) | (16u << 24) | (id << 29);
 }
 
-// 8 consecutive TMEM columns of the warp's 32 lanes
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const uint4& b) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(a.x),
-               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
-}
-
 __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_constant__ MgMaps tm,
                                                                 const __grid_constant__ MgParams p) {
   extern __shared__ uint8_t smem[];
@@ -72,23 +64,22 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
     return;
   }
   const uint32_t sbase = smem_u32(smem);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + MG_OFF_BAR);   // this CTA's copies landed
-  uint64_t* ready = full + MG_STAGES;      // even CTA: landed and scales in TMEM, in both CTAs
-  uint64_t* empty = ready + MG_STAGES;     // the pair's MMAs have read the stage
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + MG_OFF_BAR);   // even CTA: both CTAs' copies landed
+  uint64_t* empty = full + MG_STAGES;      // the pair's MMAs have read the stage
   uint64_t* accfull = empty + MG_STAGES;
   uint64_t* accempty = accfull + 1;        // even CTA: both CTAs' epilogue warps have read the accumulator
   uint64_t* mdrain = accempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int nk = (p.K + 255) / 256, KT = (p.K + 127) / 128;
   const int nN = (p.N + 255) / 256, ntiles = (p.M + 255) / 256 * nN;
   const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < MG_STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&ready[i], 8); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < MG_STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     mbar_init(accfull, 1);
     mbar_init(accempty, 16);
     mbar_init(mdrain, 1);
@@ -110,94 +101,97 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
   griddep_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t kc = 0;
-      bool ok = true;
-      for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
-        const int m0 = tile / nN * 256 + (int)rank * 128, n0 = tile % nN * 256;
-        for (int kt = 0; kt < nk; ++kt, ++kc) {
-          const int s = kc % MG_STAGES;
-          ok = (kc < (uint32_t)MG_STAGES ||
-                mbar_wait(&empty[s], (kc / MG_STAGES - 1) & 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns)) &&
-               !*abort_flag;
+    // ------------------------------------------------------------ copies
+    // both CTAs' copies count on the even CTA's barrier, which expects their sum
+    uint32_t home;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(home) : "r"(smem_u32(full)));
+    const bool one = elect_one();
+    int s = 0, ph = 0, filled = 0;   // stage, its phase, stages filled so far (up to all)
+    bool ok = true, first = true;
+    for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+      const int m0 = tile / nN * 256 + (int)rank * 128, n0 = tile % nN * 256;
+      const int sa0 = m0 / 128 * KT, sb0 = n0 / 128 * KT;
+      for (int kt = 0; kt < nk; ++kt) {
+        if (filled == MG_STAGES) {
+          ok = warp_wait(&empty[s], ph ^ 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns);
           if (!ok) break;
+        } else {
+          ++filled;
+        }
+        if (one) {
           uint8_t* st = smem + s * MG_STAGE;
-          mbar_expect_tx(&full[s], MG_STAGE + (kc == 0 ? p.inject_tx : 0u));
-          uint64_t* bar = &full[s];
-          tma_load_2d(st, &tm.a, kt * 128, m0, bar);
-          tma_load_2d(st + MG_PA, &tm.b, kt * 128, n0 + (int)rank * 128, bar);
+          if (rank == 0) mbar_expect_tx(&full[s], 2 * MG_STAGE + (first ? p.inject_tx : 0u));
+          const uint32_t bar = home + s * 8;
+          tma_load_2d_pair(st, &tm.a, kt * 128, m0, bar);
+          tma_load_2d_pair(st + MG_PA, &tm.b, kt * 128, n0 + (int)rank * 128, bar);
           // two scale tiles per 128 rows (past the end: the next rows', or zeros, not used)
-          tma_load_2d(st + MG_PA + MG_PB, &tm.sa, 0, m0 / 128 * KT + kt * 2, bar);
+          tma_load_2d_pair(st + MG_PA + MG_PB, &tm.sa, 0, sa0 + kt * 2, bar);
 #pragma unroll
           for (int b = 0; b < 2; ++b)   // each CTA multiplies all 256 weight rows
-            tma_load_2d(st + MG_PA + MG_PB + MG_SA + b * 1024, &tm.sb, 0, (n0 / 128 + b) * KT + kt * 2, bar);
+            tma_load_2d_pair(st + MG_PA + MG_PB + MG_SA + b * 1024, &tm.sb, 0, sb0 + b * KT + kt * 2, bar);
         }
+        first = false;
+        if (++s == MG_STAGES) { s = 0; ph ^= 1; }
       }
-      // the last commits arrive in this CTA's barriers: it may not leave before
-      const uint32_t c0 = kc > (uint32_t)MG_STAGES ? kc - MG_STAGES : 0;
-      for (uint32_t c = c0; c < kc && ok; ++c)
-        ok = mbar_wait(&empty[c % MG_STAGES], (c / MG_STAGES) & 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns);
-      if (!ok)   // let the copies already issued land (bounded)
-        for (uint32_t c = c0; c < kc; ++c) mbar_drain(&full[c % MG_STAGES], (c / MG_STAGES) & 1, p.wait_ns);
+    }
+    // this CTA's copies have landed once the MMAs have read them, and the last
+    // commits arrive in this CTA's barriers: it may not leave before.  (s, ph):
+    // the oldest of the stages still out, or with fewer than all filled, 0.
+    if (filled < MG_STAGES) { s = 0; ph = 1; }
+    for (int i = 0; i < filled; ++i) {
+      if (ok)
+        ok = warp_wait(&empty[s], ph ^ 1, p.status, ST_TIMEOUT_EMPTY, abort_flag, p.wait_ns);
+      if (!ok && rank == 0)   // let the pair's copies land (bounded; the odd CTA waits at the end)
+        mbar_drain(&full[s], ph ^ 1, p.wait_ns);
+      if (++s == MG_STAGES) { s = 0; ph ^= 1; }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      uint32_t kc = 0;
-      int tc = 0;
+    // ------------------------------------------------------------ MMAs
+    if (rank == 0) {
+      const bool one = elect_one();
+      int s = 0, ph = 0, acc_ph = 1;
       bool ok = true;
-      for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++tc) {
-        for (int kt = 0; kt < nk; ++kt, ++kc) {
-          const int s = kc % MG_STAGES;
-          ok = mbar_wait(&ready[s], (kc / MG_STAGES) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+      for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+        for (int kt = 0; kt < nk; ++kt) {
+          ok = warp_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = sbase + s * MG_STAGE, tsf = tmem + 256 + s * MG_SLOT_COLS;
-          if (kt == 0 && tc > 0) {
-            ok = mbar_wait(accempty, (tc - 1) & 1, p.status, ST_TIMEOUT_EPI, abort_flag, p.wait_ns);
+          const uint32_t st = sbase + s * MG_STAGE, sf = st + MG_PA + MG_PB;
+          // the scales to the stage's own TMEM columns, free again when the stage is
+          const uint32_t tsf = tmem + 256 + s * MG_SLOT_COLS;
+          if (one) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {   // 128 columns each; B: 8 TMEM columns of 256 rows
+              tc_cp2_32x128b_warpx4(tsf + q * 4, smem_desc(sf + q * 512, 16, 128, 0));
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                tc_cp2_32x128b_warpx4(tsf + 8 + q * 8 + b * 4, smem_desc(sf + MG_SA + b * 1024 + q * 512, 16, 128, 0));
+            }
+          }
+          if (kt == 0) {   // (the first tile finds the accumulator empty)
+            ok = warp_wait(accempty, acc_ph, p.status, ST_TIMEOUT_EPI, abort_flag, p.wait_ns);
             if (!ok) break;
+            acc_ph ^= 1;
             tc_fence_after();
           }
           const int kkn = min(4, p.K / 64 - kt * 4);
+          if (one) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            if (kk < kkn)
-              umma_mxf4_2(tmem, smem_desc(st + kk * 32, 16, 1024, 2), smem_desc(st + MG_PA + kk * 32, 16, 1024, 2),
-                          mg_idesc((kk & 1) * 2), tsf + (kk >> 1) * 4, tsf + 8 + (kk >> 1) * 8, kt > 0 || kk > 0);
-          tc_commit2_mc(&empty[s], 0x3);
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < kkn)
+                umma_mxf4_2(tmem, smem_desc(st + kk * 32, 16, 1024, 2), smem_desc(st + MG_PA + kk * 32, 16, 1024, 2),
+                            mg_idesc((kk & 1) * 2), tsf + (kk >> 1) * 4, tsf + 8 + (kk >> 1) * 8, kt > 0 || kk > 0);
+            tc_commit2_mc(&empty[s], 0x3);
+            if (kt == nk - 1) tc_commit2_mc(accfull, 0x3);
+          }
+          if (++s == MG_STAGES) { s = 0; ph ^= 1; }
         }
-        if (ok) tc_commit2_mc(accfull, 0x3);
       }
       if (!ok) {   // wait (bounded) for the MMAs already issued
-        tc_commit2_mc(mdrain, 0x1);
+        if (one) tc_commit2_mc(mdrain, 0x1);
         mbar_drain(mdrain, 0, p.wait_ns);
       }
     }
-  } else if (warp >= 12) {
-    // ------------------------------------------------------------ scales -> TMEM
-    // one warp per lane quadrant: every quadrant holds the same 32 rows x 24
-    // columns, word (l, c) of a tile the scale bytes of row 32 c + l
-    const uint32_t quad = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256;
-    uint32_t kc = 0;
-    bool ok = true;
-    for (int tile = tile0; tile < ntiles && ok; tile += tstep)
-      for (int kt = 0; kt < nk; ++kt, ++kc) {
-        const int s = kc % MG_STAGES;
-        ok = mbar_wait(&full[s], (kc / MG_STAGES) & 1, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
-        if (!ok) break;
-        tc_fence_after();   // (the stage's columns are free: its MMAs were done before it was filled again)
-        const uint4* sf = reinterpret_cast<const uint4*>(smem + s * MG_STAGE + MG_PA + MG_PB) + lane;
-        uint4 w[6];   // A: 2 x 128 columns; B: 2 x 128 columns of two row tiles
-        w[0] = sf[0]; w[1] = sf[32];
-        w[2] = sf[64]; w[3] = sf[128];
-        w[4] = sf[96]; w[5] = sf[160];
-        tmem_st8(quad + s * MG_SLOT_COLS, w[0], w[1]);
-        tmem_st8(quad + s * MG_SLOT_COLS + 8, w[2], w[3]);
-        tmem_st8(quad + s * MG_SLOT_COLS + 16, w[4], w[5]);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(&ready[s], 0);
-      }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
