@@ -149,9 +149,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
   float* part = reinterpret_cast<float*>(smem);       // [NA][NT][FEW_PITCH], over the stages once they are used up
 
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
   uint32_t S;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+  S = (uint32_t)uniform((int)S);
+  const uint32_t rank = (uint32_t)uniform((int)cluster_ctarank());
   const int tile = (int)(blockIdx.x / S), n0 = tile * 128;
 
   if (threadIdx.x == 0) {
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   if (!p.early) griddep_wait();
 
   // this rank's steps of 256 columns: [s0, s0 + n)
@@ -178,11 +179,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
   int total = spe, expert = 0;
   bool live = true;
   if constexpr (MODE != LINEAR) {
-    const int na = list_active(p.idx, p.T * p.top_k, bits, act);
+    const int na = uniform(list_active(p.idx, p.T * p.top_k, bits, act));
     if constexpr (MODE == GATE_UP) {
       griddep_launch_dependents();   // every CTA of this grid has seen the routing by now
       live = (int)blockIdx.y < na;
-      if (live) expert = act[blockIdx.y];
+      if (live) expert = uniform(act[blockIdx.y]);
     } else {
       total = na * spe;
     }
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
       if (++q.kt == spe) { q.kt = 0; ++q.a; }
     };
     auto load = [&](const Pos& q, bool first, bool wt, bool tk) {
-      const int e = MODE == DOWN ? __shfl_sync(0xffffffffu, (int)act[q.a], 0) : expert;
+      const int e = MODE == DOWN ? uniform(act[q.a]) : expert;
       if (!one) return;
       uint64_t* bar = &full[q.s];
       uint8_t* s = smem + q.s * STAGE;

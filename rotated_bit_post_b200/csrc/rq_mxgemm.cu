@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
 
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = (uint32_t)uniform((int)cluster_ctarank());
   const int nk = (p.K + 255) / 256, KT = (p.K + 127) / 128;
   const int nN = (p.N + 255) / 256, ntiles = (p.M + 255) / 256 * nN;
   const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
   tc_fence_before();
   cluster_sync();   // both CTAs' barriers exist before either arrives on the other's
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   griddep_wait();
 
   if (warp == 0) {
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
     // both CTAs' copies count on the even CTA's barrier, which expects their sum
     uint32_t home;
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(home) : "r"(smem_u32(full)));
+    home = (uint32_t)uniform((int)home);
     const bool one = elect_one();
     int s = 0, ph = 0, filled = 0;   // stage, its phase, stages filled so far (up to all)
     bool ok = true, first = true;

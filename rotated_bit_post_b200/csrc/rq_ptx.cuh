@@ -114,7 +114,10 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+// A value that is the same in every lane, in a form the compiler knows to be so
+// (what comes from shared memory or a special register is not, to it).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int uniform_warp() { return uniform((int)(threadIdx.x >> 5)); }
 // mbar_wait by all lanes of a warp, one answer for all.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status, int32_t code,
                                           volatile int32_t* abort_flag, uint64_t limit_ns) {
