@@ -40,7 +40,7 @@ namespace {
 constexpr int FEW_THREADS = 256;
 constexpr int FEW_MAX_STAGES = 8;
 constexpr int FEW_PITCH = 132;          // floats between tokens of the partial sums (16-byte rows, no bank repeats)
-constexpr int FEW_TAIL = 1024;          // barriers, TMEM address, active experts
+constexpr int FEW_TAIL = 2048;          // barriers, TMEM address, active experts, the expert's tokens
 
 struct __align__(64) FewMaps {
   CUtensorMap w;   // weight codes, all experts' rows one after another
@@ -96,24 +96,24 @@ __device__ __forceinline__ void few_tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 }
 
 // Ascending list of the experts that some token chose, in act[]; its length.
-// bits: 8 words of shared scratch.  Called by the whole CTA.
-__device__ int list_active(const int32_t* idx, int n, uint32_t* bits, uint16_t* act) {
-  if (threadIdx.x < 8) bits[threadIdx.x] = 0u;
+// flag: 256 bytes, words: 8 words of shared scratch.  Called by the whole CTA.
+__device__ int list_active(const int32_t* idx, int n, uint8_t* flag, uint32_t* words, uint16_t* act) {
+  const int e = (int)threadIdx.x;   // 256 threads, one expert each
+  flag[e] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += FEW_THREADS) {
-    const uint32_t e = (uint32_t)__ldcg(idx + i) & 255u;
-    atomicOr(&bits[e >> 5], 1u << (e & 31));
-  }
+  for (int i = e; i < n; i += FEW_THREADS) flag[__ldcg(idx + i) & 255] = 1;
+  __syncthreads();
+  const uint32_t w = __ballot_sync(0xffffffffu, flag[e]);
+  if ((e & 31) == 0) words[e >> 5] = w;
   __syncthreads();
   int before = 0, all = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int c = __popc(bits[i]);
-    before += i < ((int)threadIdx.x >> 5) ? c : 0;
+    const int c = __popc(words[i]);
+    before += i < (e >> 5) ? c : 0;
     all += c;
   }
-  const uint32_t w = bits[threadIdx.x >> 5], lane = threadIdx.x & 31;   // 256 threads, one expert each
-  if (w >> lane & 1u) act[before + __popc(w & ((1u << lane) - 1u))] = (uint16_t)threadIdx.x;
+  if (flag[e]) act[before + __popc(w & ((1u << (e & 31)) - 1u))] = (uint16_t)e;
   __syncthreads();
   return all;
 }
@@ -144,8 +144,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
   uint64_t* mdrain = accfull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
-  uint32_t* bits = tmem_slot + 4;
-  uint16_t* act = reinterpret_cast<uint16_t*>(bits + 8);
+  uint32_t* words = tmem_slot + 4;
+  uint16_t* act = reinterpret_cast<uint16_t*>(words + 8);
+  uint8_t* flag = reinterpret_cast<uint8_t*>(act + 256);   // GATE_UP reuses it: the tokens that chose the expert
+  float* wsel = reinterpret_cast<float*>(flag + 256);      // and their weights
   float* part = reinterpret_cast<float*>(smem);       // [NA][NT][FEW_PITCH], over the stages once they are used up
 
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
   int total = spe, expert = 0;
   bool live = true;
   if constexpr (MODE != LINEAR) {
-    const int na = uniform(list_active(p.idx, p.T * p.top_k, bits, act));
+    const int na = uniform(list_active(p.idx, p.T * p.top_k, flag, words, act));
     if constexpr (MODE == GATE_UP) {
       griddep_launch_dependents();   // every CTA of this grid has seen the routing by now
       live = (int)blockIdx.y < na;
@@ -245,12 +247,17 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
       const bool one = elect_one();
       bool ok = true;
       int s = 0, ph = 0, kt = s0 % spe;
+      // descriptors of the first stage; the address field counts 16-byte units,
+      // so everything else is one addition (rebuilding them for every
+      // instruction took 150 of 550 cycles a step)
+      const uint64_t d_op = smem_desc(sbase, 16, 1024, 2), d_sf = smem_desc(sbase + NA * PA + PB, 16, 128, 0);
+      const uint32_t id0 = few_idesc(p.NT, 0), id2 = few_idesc(p.NT, 2);
       for (int i = 0; i < n; ++i) {
         ok = warp_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
         const int sct = min(2, KT - kt * 2), kkn = min(4, p.K / 64 - kt * 4);
-        const uint32_t st = sbase + s * STAGE;
+        const uint32_t st = (uint32_t)(s * STAGE) >> 4;
         // a slot of scale columns per stage: free again when the stage is
         const uint32_t tsf = tmem + NA * p.NT + s * (NA + 1) * 8;
         if (one) {
@@ -259,16 +266,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
             if (q < sct) {
 #pragma unroll
               for (int h = 0; h <= NA; ++h)   // weight scales, then the tokens'
-                tc_cp_32x128b_warpx4(tsf + h * 8 + q * 4, smem_desc(st + NA * PA + PB + h * SF + q * 512, 16, 128, 0));
+                tc_cp_32x128b_warpx4(tsf + h * 8 + q * 4, d_sf + st + ((h * SF + q * 512) >> 4));
             }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             if (kk < kkn) {
 #pragma unroll
               for (int h = 0; h < NA; ++h)
-                umma_mxf4(tmem + h * p.NT, smem_desc(st + h * PA + kk * 32, 16, 1024, 2),
-                          smem_desc(st + NA * PA + kk * 32, 16, 1024, 2), few_idesc(p.NT, (kk & 1) * 2),
-                          tsf + h * 8 + (kk >> 1) * 4, tsf + NA * 8 + (kk >> 1) * 4, i > 0 || kk > 0);
+                umma_mxf4(tmem + h * p.NT, d_op + st + ((h * PA + kk * 32) >> 4), d_op + st + ((NA * PA + kk * 32) >> 4),
+                          kk & 1 ? id2 : id0, tsf + h * 8 + (kk >> 1) * 4, tsf + NA * 8 + (kk >> 1) * 4, i > 0 || kk > 0);
             }
           tc_commit(&empty[s]);
           if (i == n - 1) tc_commit(accfull);
@@ -279,6 +285,28 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
       if (!ok) {   // wait (bounded) for the MMAs already issued
         if (one) tc_commit(mdrain);
         mbar_drain(mdrain, 0, p.wait_ns);
+      }
+    }
+  } else if (MODE == GATE_UP && warp < 4) {
+    // ------------------------------------------------------------ the expert's tokens
+    // while the weights stream: whether each token chose the expert and its
+    // weight, and zeros (codes and scale bytes) into this tile's hidden rows of
+    // the others; each rank of the cluster the tokens t % S
+    const int t = (warp - 2) * 32 + lane;
+    if (t < 64) {
+      uint8_t hit = 0;
+      if (live && t < p.T)
+        for (int j = 0; j < p.top_k; ++j)
+          if (__ldcg(p.idx + t * p.top_k + j) == expert) {
+            hit = 1;
+            wsel[t] = __ldcg(p.wts + t * p.top_k + j);
+          }
+      flag[t] = hit;
+      if (live && t < p.T && !hit && t % (int)S == (int)rank) {
+        uint4* row = reinterpret_cast<uint4*>(p.hq + ((size_t)blockIdx.y * p.T + t) * (p.N / 2) + n0 / 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint32_t*>(p.hq_sf + (size_t)blockIdx.y * (p.N / 128) * 512 + mx_sf_offset(t, n0 / 32, p.N)) = 0u;
       }
     }
   } else if (warp >= 4) {
@@ -320,30 +348,26 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
     };
     for (int t = (int)rank + warp * (int)S; t < p.T; t += (int)S * (FEW_THREADS / 32)) {
       if constexpr (MODE == GATE_UP) {
-        // the token's weight for this expert, if it chose it
-        const bool hit = lane < p.top_k && __ldcg(p.idx + t * p.top_k + min(lane, p.top_k - 1)) == expert;
-        const uint32_t who = __ballot_sync(0xffffffffu, hit);
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (who) {
-          const float w = __ldcg(p.wts + t * p.top_k + __ffs(who) - 1);
-          const float4 g = sum(t), u = sum(p.NT + t);
-          const float gg[4] = {g.x, g.y, g.z, g.w}, uu[4] = {u.x, u.y, u.z, u.w};
+        if (!flag[t]) continue;
+        float v[4];
+        const float w = wsel[t];
+        const float4 g = sum(t), u = sum(p.NT + t);
+        const float gg[4] = {g.x, g.y, g.z, g.w}, uu[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = __fmul_rn(w, __fmul_rn(__fdiv_rn(gg[i], __fadd_rn(1.f, expf(-gg[i]))), uu[i]));
-          // channels 4 lane .. 4 lane + 3: strides 1 and 2 here, 4 .. across lanes
-          float a = v[0], b = v[2];
-          v[0] = __fadd_rn(a, v[1]); v[1] = __fsub_rn(a, v[1]);
-          v[2] = __fadd_rn(b, v[3]); v[3] = __fsub_rn(b, v[3]);
-          a = v[0]; b = v[1];
-          v[0] = __fadd_rn(a, v[2]); v[2] = __fsub_rn(a, v[2]);
-          v[1] = __fadd_rn(b, v[3]); v[3] = __fsub_rn(b, v[3]);
-          for (int m = 1; m < p.block2 / 4; m <<= 1) {
+        for (int i = 0; i < 4; ++i)
+          v[i] = __fmul_rn(w, __fmul_rn(__fdiv_rn(gg[i], __fadd_rn(1.f, expf(-gg[i]))), uu[i]));
+        // channels 4 lane .. 4 lane + 3: strides 1 and 2 here, 4 .. across lanes
+        float a = v[0], b = v[2];
+        v[0] = __fadd_rn(a, v[1]); v[1] = __fsub_rn(a, v[1]);
+        v[2] = __fadd_rn(b, v[3]); v[3] = __fsub_rn(b, v[3]);
+        a = v[0]; b = v[1];
+        v[0] = __fadd_rn(a, v[2]); v[2] = __fsub_rn(a, v[2]);
+        v[1] = __fadd_rn(b, v[3]); v[3] = __fsub_rn(b, v[3]);
+        for (int m = 1; m < p.block2 / 4; m <<= 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float o = __shfl_xor_sync(0xffffffffu, v[i], m);
-              v[i] = lane & m ? __fsub_rn(o, v[i]) : __fadd_rn(v[i], o);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float o = __shfl_xor_sync(0xffffffffu, v[i], m);
+            v[i] = lane & m ? __fsub_rn(o, v[i]) : __fadd_rn(v[i], o);
           }
         }
         float am = 0.f;

@@ -152,21 +152,23 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
       const bool one = elect_one();
       int s = 0, ph = 0, acc_ph = 1;
       bool ok = true;
+      // descriptors of the first stage; the address field counts 16-byte units
+      const uint64_t d_op = smem_desc(sbase, 16, 1024, 2), d_sf = smem_desc(sbase + MG_PA + MG_PB, 16, 128, 0);
       for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
         for (int kt = 0; kt < nk; ++kt) {
           ok = warp_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = sbase + s * MG_STAGE, sf = st + MG_PA + MG_PB;
+          const uint32_t st = (uint32_t)(s * MG_STAGE) >> 4;
           // the scales to the stage's own TMEM columns, free again when the stage is
           const uint32_t tsf = tmem + 256 + s * MG_SLOT_COLS;
           if (one) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {   // 128 columns each; B: 8 TMEM columns of 256 rows
-              tc_cp2_32x128b_warpx4(tsf + q * 4, smem_desc(sf + q * 512, 16, 128, 0));
+              tc_cp2_32x128b_warpx4(tsf + q * 4, d_sf + st + ((q * 512) >> 4));
 #pragma unroll
               for (int b = 0; b < 2; ++b)
-                tc_cp2_32x128b_warpx4(tsf + 8 + q * 8 + b * 4, smem_desc(sf + MG_SA + b * 1024 + q * 512, 16, 128, 0));
+                tc_cp2_32x128b_warpx4(tsf + 8 + q * 8 + b * 4, d_sf + st + ((MG_SA + b * 1024 + q * 512) >> 4));
             }
           }
           if (kt == 0) {   // (the first tile finds the accumulator empty)
@@ -180,8 +182,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               if (kk < kkn)
-                umma_mxf4_2(tmem, smem_desc(st + kk * 32, 16, 1024, 2), smem_desc(st + MG_PA + kk * 32, 16, 1024, 2),
-                            mg_idesc((kk & 1) * 2), tsf + (kk >> 1) * 4, tsf + 8 + (kk >> 1) * 8, kt > 0 || kk > 0);
+                umma_mxf4_2(tmem, d_op + st + ((kk * 32) >> 4), d_op + st + ((MG_PA + kk * 32) >> 4), mg_idesc((kk & 1) * 2),
+                            tsf + (kk >> 1) * 4, tsf + 8 + (kk >> 1) * 8, kt > 0 || kk > 0);
             tc_commit2_mc(&empty[s], 0x3);
             if (kt == nk - 1) tc_commit2_mc(accfull, 0x3);
           }
