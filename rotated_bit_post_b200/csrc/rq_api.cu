@@ -450,6 +450,23 @@ rq_status rq_mxfp4_layer(int32_t M, int32_t N, int32_t K, int32_t block, const u
   if (!workspace || !w_codes || !w_bscale || !Y) return fail(RQ_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(workspace) || !aligned16(w_codes) || !aligned16(w_bscale) || !aligned16(Y))
     return fail(RQ_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+  const int sms = num_sms();
+  if (rq::mx_layer_fused(M, N, K, sms)) {
+    if (!X || !rot) return fail(RQ_ERR_INVALID_ARG, "null input/output pointer");
+    if (!aligned16(X) || !aligned16(rot)) return fail(RQ_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    rq::GemmLaunch g{};
+    g.M = M; g.N = N; g.K = K;
+    g.w_codes = w_codes; g.w_bscale = w_bscale;
+    g.Y = Y; g.out_fp32 = out_fp32 ? 1 : 0;
+    g.status = status;
+    g.num_sms = sms;
+    g.wait_ns = g_wait_ns.load();
+    g.inject_tx = g_inject_tx.load();
+    const cudaError_t e = rq::launch_mx_layer_fused(g, X, rot, block, (float)(1.0 / std::sqrt((double)block)),
+                                                    static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(RQ_ERR_CUDA, "layer launch failed: %s", cudaGetErrorString(e));
+    return ok();
+  }
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   uint8_t* bscale = codes + up256((int64_t)M * (K / 2));
   s = run_k1(RQ_MXFP4, false, X, M, K, block, rot, nullptr, nullptr, 0, nullptr, codes, nullptr, bscale,

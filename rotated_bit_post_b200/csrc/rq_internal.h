@@ -145,6 +145,10 @@ cudaError_t launch_mx_gemm(const GemmLaunch& a, cudaStream_t st, const char** wh
 // MXFP4 products of at most MX_FEW_TOKENS tokens (rq_mxfew.cu)
 constexpr int MX_FEW_TOKENS = 64;
 cudaError_t launch_mx_few(const GemmLaunch& a, cudaStream_t st, const char** why);
+// the whole layer from BF16 rows in one launch, for the shapes it takes
+bool mx_layer_fused(int M, int N, int K, int sms);
+cudaError_t launch_mx_layer_fused(const GemmLaunch& a, const uint16_t* x, const int32_t* rot, int block, float inv_sqrt_b,
+                                  cudaStream_t st);
 // gate/up and down products of an expert layer whose routing and activation
 // codes are in place; `active`: the most experts that T tokens can choose
 cudaError_t launch_moe_products(const MoeLaunch& a, const uint8_t* xq, const uint8_t* xq_sf, uint8_t* hq, uint8_t* hq_sf,

@@ -45,58 +45,6 @@ struct PrepParams {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// One warp transforms and quantizes 32 EPL rotated coordinates of row m from
-// `base`, EPL consecutive ones per lane, from the row staged in shared memory:
-// butterflies in ascending stride, inside the lane and then across lanes.
-template <int EPL>
-__device__ __forceinline__ void rotate_unit(const uint16_t* xs, const int32_t* rot, int base, int block, float isb, int m,
-                                            int K, uint8_t* codes, uint8_t* sf) {
-  const int lane = threadIdx.x & 31, k0 = base + lane * EPL;
-  float v[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int32_t r = __ldg(rot + k0 + i);
-    v[i] = __uint_as_float(((uint32_t)xs[r & 0x7fffffff] << 16) ^ ((uint32_t)r & 0x80000000u));
-  }
-#pragma unroll
-  for (int h = 1; h < EPL; h <<= 1) {   // EPL <= block unless it is 1
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (!(i & h)) {
-        const float a = v[i], b = v[i + h];
-        v[i] = __fadd_rn(a, b);
-        v[i + h] = __fsub_rn(a, b);
-      }
-  }
-  for (int s = 1; s * EPL < block; s <<= 1) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const float o = __shfl_xor_sync(0xffffffffu, v[i], s);
-      v[i] = lane & s ? __fsub_rn(o, v[i]) : __fadd_rn(v[i], o);
-    }
-  }
-  float am = 0.f;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    v[i] = __fmul_rn(v[i], isb);
-    am = fmax_nan(am, fabsf(v[i]));
-  }
-#pragma unroll
-  for (int s = 1; s < 32 / EPL; s <<= 1) am = fmax_nan(am, __shfl_xor_sync(0xffffffffu, am, s));
-  const uint32_t sb = mx_scale_byte(am);
-  const float inv = mx_inv_scale(sb);
-  uint8_t* dst = codes + (size_t)m * (K / 2) + k0 / 2;
-  if constexpr (EPL == 1) {
-    const float y = __fmul_rn(v[0], inv), up = __shfl_down_sync(0xffffffffu, y, 1);
-    if (!(lane & 1)) *dst = sb == 255u ? (uint8_t)0 : cvt_e2m1x2(up, y);
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPL; i += 2)
-      dst[i / 2] = sb == 255u ? (uint8_t)0 : cvt_e2m1x2(__fmul_rn(v[i + 1], inv), __fmul_rn(v[i], inv));
-  }
-  if (k0 % 32 == 0) sf[mx_sf_offset(m, k0 / 32, K)] = (uint8_t)sb;
-}
-
 // A logit as an unsigned key of the same order: -0 as +0, NaN as -infinity,
 // never 0 (the key of an expert that is taken or does not exist).
 __device__ __forceinline__ uint32_t logit_key(float l) {
@@ -137,17 +85,15 @@ __global__ void __launch_bounds__(PREP_THREADS) __cluster_dims__(PREP_CLUSTER, 1
     for (int m = 16; m; m >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, m);
     if (lane == 0) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(home + e * 4), "f"(s0) : "memory");
   }
+  const auto sink = [&](int k, uint8_t*& codes, uint8_t*& sf) {
+    codes = p.xq + (size_t)t * (p.K / 2) + k / 2;
+    sf = p.xq_sf + mx_sf_offset(t, k / 32, p.K);
+    return true;
+  };
   // rotated blocks, `unit` coordinates (whole Hadamard blocks) per warp and turn
   const int unit = p.block < 32 ? 32 : p.block;
   for (int u = rank + warp * PREP_CLUSTER; u < p.K / unit; u += PREP_CLUSTER * (PREP_THREADS / 32)) {
-    switch (unit) {
-      case 32: rotate_unit<1>(xs, p.rot, u * 32, p.block, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
-      case 64: rotate_unit<2>(xs, p.rot, u * 64, 64, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
-      case 128: rotate_unit<4>(xs, p.rot, u * 128, 128, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
-      case 256: rotate_unit<8>(xs, p.rot, u * 256, 256, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
-      case 512: rotate_unit<16>(xs, p.rot, u * 512, 512, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
-      default: rotate_unit<32>(xs, p.rot, u * 1024, 1024, p.inv_sqrt_b, t, p.K, p.xq, p.xq_sf); break;
-    }
+    mx_rotate_unit(xs, p.rot + u * unit, u * unit, p.block, p.inv_sqrt_b, sink);
   }
   cluster_sync();
   if (rank != 0 || warp != 0) return;

@@ -5,6 +5,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "rq_ptx.cuh"
+
 namespace rq {
 
 // Scale byte (m, kb), kb = k / 32: tile (m / 128, kb / 4), inside it
@@ -45,6 +47,81 @@ __device__ __forceinline__ float e2m1_value(uint32_t n) {
   const uint32_t m = n & 7u;
   const float a = m < 2u ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
   return n & 8u ? -a : a;
+}
+
+// One warp transforms and quantizes 32 EPL rotated coordinates from `base` on, EPL
+// consecutive ones per lane, of the BF16 row xs (shared memory): butterflies in
+// ascending stride, inside the lane and then across lanes.  rot: the table's
+// entries from `base` on.  sink(k, codes, sf) says where coordinate k's packed
+// codes and its block's scale byte go, or false for nowhere.
+template <int EPL, class Sink>
+__device__ __forceinline__ void mx_rotate_epl(const uint16_t* xs, const int32_t* rot, int base, int block, float isb,
+                                              const Sink& sink) {
+  const int lane = threadIdx.x & 31, k0 = base + lane * EPL;
+  float v[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int32_t r = rot[lane * EPL + i];
+    v[i] = __uint_as_float(((uint32_t)xs[r & 0x7fffffff] << 16) ^ ((uint32_t)r & 0x80000000u));
+  }
+#pragma unroll
+  for (int h = 1; h < EPL; h <<= 1) {   // EPL <= block unless it is 1
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (!(i & h)) {
+        const float a = v[i], b = v[i + h];
+        v[i] = __fadd_rn(a, b);
+        v[i + h] = __fsub_rn(a, b);
+      }
+  }
+  for (int s = 1; s * EPL < block; s <<= 1) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float o = __shfl_xor_sync(0xffffffffu, v[i], s);
+      v[i] = lane & s ? __fsub_rn(o, v[i]) : __fadd_rn(v[i], o);
+    }
+  }
+  float am = 0.f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    v[i] = __fmul_rn(v[i], isb);
+    am = fmax_nan(am, fabsf(v[i]));
+  }
+#pragma unroll
+  for (int s = 1; s < 32 / EPL; s <<= 1) am = fmax_nan(am, __shfl_xor_sync(0xffffffffu, am, s));
+  const uint32_t sb = mx_scale_byte(am);
+  const float inv = mx_inv_scale(sb);
+  float up = 0.f;
+  if constexpr (EPL == 1) up = __shfl_down_sync(0xffffffffu, __fmul_rn(v[0], inv), 1);
+  uint8_t *dst, *sf;
+  if (!sink(k0, dst, sf)) return;
+  if constexpr (EPL == 1) {
+    if (!(lane & 1)) *dst = sb == 255u ? (uint8_t)0 : cvt_e2m1x2(up, __fmul_rn(v[0], inv));
+  } else {
+    uint32_t w[(EPL + 7) / 8];
+#pragma unroll
+    for (int i = 0; i < (EPL + 7) / 8; ++i) w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < EPL; i += 2)
+      w[i / 8] |= (sb == 255u ? 0u : (uint32_t)cvt_e2m1x2(__fmul_rn(v[i + 1], inv), __fmul_rn(v[i], inv))) << (4 * (i & 7));
+    if constexpr (EPL == 2) *dst = (uint8_t)w[0];
+    else if constexpr (EPL == 4) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w[0];
+    else if constexpr (EPL == 8) *reinterpret_cast<uint32_t*>(dst) = w[0];
+    else if constexpr (EPL == 16) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (k0 % 32 == 0) *sf = (uint8_t)sb;
+}
+// The same for max(block, 32) coordinates, whole Hadamard blocks.
+template <class Sink>
+__device__ __forceinline__ void mx_rotate_unit(const uint16_t* xs, const int32_t* rot, int base, int block, float isb,
+                                               const Sink& sink) {
+  if (block <= 32) mx_rotate_epl<1>(xs, rot, base, block, isb, sink);
+  else if (block == 64) mx_rotate_epl<2>(xs, rot, base, 64, isb, sink);
+  else if (block == 128) mx_rotate_epl<4>(xs, rot, base, 128, isb, sink);
+  else if (block == 256) mx_rotate_epl<8>(xs, rot, base, 256, isb, sink);
+  else if (block == 512) mx_rotate_epl<16>(xs, rot, base, 512, isb, sink);
+  else mx_rotate_epl<32>(xs, rot, base, 1024, isb, sink);
 }
 
 }  // namespace rq

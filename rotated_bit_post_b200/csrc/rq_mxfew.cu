@@ -8,8 +8,11 @@
 // which join their FP32 partial sums through distributed shared memory, always
 // in rank order.
 //
-// One mainloop, three uses:
+// One mainloop, four uses:
 //   LINEAR   Y[t, n] = sum_k W[n, k] x[t, k] (+ c L^T)
+//   FUSED    the same from BF16 rows: each CTA transforms and quantizes its own
+//            part of the rows while the weights are on their way, which costs
+//            less than a launch of its own (a few thousand values per CTA)
 //   GATE_UP  one active expert and 128 hidden channels per cluster: two
 //            accumulators (gate rows, up rows); h = w silu(g) u, the block
 //            Hadamard transform and the MXFP4 quantization of the hidden rows in
@@ -68,6 +71,10 @@ struct FewParams {
   uint8_t *hq, *hq_sf;     // hidden rows out (GATE_UP)
   int block2;
   float inv_sqrt_b2;
+  const uint16_t* xb;      // FUSED: T x K BF16 rows, their rotation, offsets in shared memory of the
+  const int32_t* rot;      // codes of all steps (the scales behind them), rows and table entries
+  int block, off_x, off_rows, off_rot;
+  float inv_sqrt_b;
   int32_t* status;
   uint64_t wait_ns;
   uint32_t inject_tx;
@@ -124,7 +131,10 @@ __device__ __forceinline__ uint32_t few_idesc(int n, uint32_t id) {
   return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (8u << 24) | (id << 29);
 }
 
-enum { LINEAR = 0, GATE_UP = 1, DOWN = 2 };
+enum { LINEAR = 0, GATE_UP = 1, DOWN = 2, FUSED = 3 };
+constexpr int FUSED_SF = 512;           // FUSED: scale bytes per step, two tiles 256 bytes apart: the rows past
+                                        // the 16th that a tile's copy also brings are other tiles', not used
+constexpr int FUSED_WARPS = 6;          // warps 2-7 transform the rows
 
 template <int MODE>
 __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_constant__ FewMaps tm,
@@ -135,14 +145,16 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
   const int PB = p.NT * 128;
-  const int STAGE = NA * (PA + SF) + PB + SF;
+  constexpr bool EXPERTS = MODE == GATE_UP || MODE == DOWN;
+  const int STAGE = NA * (PA + SF) + (MODE == FUSED ? 0 : PB + SF);
   // stage: [NA] weight codes | token codes | [NA] weight scales | token scales
   uint8_t* tail = smem + p.tail;
   uint64_t* full = reinterpret_cast<uint64_t*>(tail);
   uint64_t* empty = full + FEW_MAX_STAGES;
   uint64_t* accfull = empty + FEW_MAX_STAGES;
   uint64_t* mdrain = accfull + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
+  uint64_t* xready = mdrain + 1;          // FUSED: the rows are quantized
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xready + 1);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
   uint32_t* words = tmem_slot + 4;
   uint16_t* act = reinterpret_cast<uint16_t*>(words + 8);
@@ -161,10 +173,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
     for (int i = 0; i < p.stages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     mbar_init(accfull, 1);
     mbar_init(mdrain, 1);
+    mbar_init(xready, FUSED_WARPS);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm.w);
-    prefetch_tmap(&tm.x);
+    if (MODE != FUSED) prefetch_tmap(&tm.x);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem_cols);
@@ -180,7 +193,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
   const int spe = (p.K + 255) / 256, KT = (p.K + 127) / 128;
   int total = spe, expert = 0;
   bool live = true;
-  if constexpr (MODE != LINEAR) {
+  if constexpr (EXPERTS) {
     const int na = uniform(list_active(p.idx, p.T * p.top_k, flag, words, act));
     if constexpr (MODE == GATE_UP) {
       griddep_launch_dependents();   // every CTA of this grid has seen the routing by now
@@ -210,16 +223,16 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
       uint8_t* s = smem + q.s * STAGE;
       const uint32_t sfb = (uint32_t)min(2, KT - q.kt * 2) * 512;   // scale bytes of 128 rows
       if (wt) {
-        mbar_expect_tx(bar, NA * (PA + sfb) + PB + sfb + (first ? p.inject_tx : 0u));
-        const uint8_t* sf = p.w_sf + (MODE == LINEAR ? 0 : (size_t)e * p.w_sf_expert) + (size_t)q.kt * 1024;
+        mbar_expect_tx(bar, NA * (PA + sfb) + (MODE == FUSED ? 0 : PB + sfb) + (first ? p.inject_tx : 0u));
+        const uint8_t* sf = p.w_sf + (EXPERTS ? (size_t)e * p.w_sf_expert : 0) + (size_t)q.kt * 1024;
 #pragma unroll
         for (int h = 0; h < NA; ++h) {   // GATE_UP: rows I..2I-1 are the up rows
-          const int row = (MODE == LINEAR ? 0 : e * NA * p.N) + h * p.N + n0;
+          const int row = (EXPERTS ? e * NA * p.N : 0) + h * p.N + n0;
           tma_load_2d(s + h * PA, &tm.w, q.kt * 128, row, bar);
-          bulk_g2s(s + NA * PA + PB + h * SF, sf + (size_t)h * (p.N / 128) * KT * 512 + rowt, sfb, bar);
+          bulk_g2s(s + NA * PA + (MODE == FUSED ? 0 : PB) + h * SF, sf + (size_t)h * (p.N / 128) * KT * 512 + rowt, sfb, bar);
         }
       }
-      if (tk) {
+      if (MODE != FUSED && tk) {
         const int a = MODE == DOWN ? q.a : 0;
         tma_load_2d(s + NA * PA, &tm.x, q.kt * 128, a * p.T, bar);
         bulk_g2s(s + NA * (PA + SF) + PB, p.x_sf + (size_t)a * KT * 512 + (size_t)q.kt * 1024, sfb, bar);
@@ -250,14 +263,19 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
       // descriptors of the first stage; the address field counts 16-byte units,
       // so everything else is one addition (rebuilding them for every
       // instruction took 150 of 550 cycles a step)
-      const uint64_t d_op = smem_desc(sbase, 16, 1024, 2), d_sf = smem_desc(sbase + NA * PA + PB, 16, 128, 0);
+      const uint64_t d_op = smem_desc(sbase, 16, 1024, 2), d_sf = smem_desc(sbase + NA * PA + (MODE == FUSED ? 0 : PB), 16, 128, 0);
+      const uint64_t d_x = smem_desc(sbase + (MODE == FUSED ? p.off_x : NA * PA), 16, 1024, 2);
+      const uint64_t d_xsf = smem_desc(sbase + (MODE == FUSED ? p.off_x + n * PB : NA * PA + PB + NA * SF), 16, 128, 0);
+      if (MODE == FUSED) ok = warp_wait(xready, 0, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
       const uint32_t id0 = few_idesc(p.NT, 0), id2 = few_idesc(p.NT, 2);
-      for (int i = 0; i < n; ++i) {
+      for (int i = 0; i < n && ok; ++i) {
         ok = warp_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
         const int sct = min(2, KT - kt * 2), kkn = min(4, p.K / 64 - kt * 4);
         const uint32_t st = (uint32_t)(s * STAGE) >> 4;
+        const uint32_t xst = MODE == FUSED ? (uint32_t)(i * PB) >> 4 : st;          // token codes and scales:
+        const uint32_t xsf = MODE == FUSED ? (uint32_t)(i * FUSED_SF) >> 4 : st;    // of every step, or the stage's
         // a slot of scale columns per stage: free again when the stage is
         const uint32_t tsf = tmem + NA * p.NT + s * (NA + 1) * 8;
         if (one) {
@@ -265,15 +283,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
           for (int q = 0; q < 2; ++q)
             if (q < sct) {
 #pragma unroll
-              for (int h = 0; h <= NA; ++h)   // weight scales, then the tokens'
-                tc_cp_32x128b_warpx4(tsf + h * 8 + q * 4, d_sf + st + ((h * SF + q * 512) >> 4));
+              for (int h = 0; h < NA; ++h) tc_cp_32x128b_warpx4(tsf + h * 8 + q * 4, d_sf + st + ((h * SF + q * 512) >> 4));
+              tc_cp_32x128b_warpx4(tsf + NA * 8 + q * 4, d_xsf + xsf + ((q * (MODE == FUSED ? 256 : 512)) >> 4));
             }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             if (kk < kkn) {
 #pragma unroll
               for (int h = 0; h < NA; ++h)
-                umma_mxf4(tmem + h * p.NT, d_op + st + ((h * PA + kk * 32) >> 4), d_op + st + ((NA * PA + kk * 32) >> 4),
+                umma_mxf4(tmem + h * p.NT, d_op + st + ((h * PA + kk * 32) >> 4), d_x + xst + ((kk * 32) >> 4),
                           kk & 1 ? id2 : id0, tsf + h * 8 + (kk >> 1) * 4, tsf + NA * 8 + (kk >> 1) * 4, i > 0 || kk > 0);
             }
           tc_commit(&empty[s]);
@@ -309,7 +327,39 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
         *reinterpret_cast<uint32_t*>(p.hq_sf + (size_t)blockIdx.y * (p.N / 128) * 512 + mx_sf_offset(t, n0 / 32, p.N)) = 0u;
       }
     }
-  } else if (warp >= 4) {
+  }
+  if constexpr (MODE == FUSED) {
+    if (warp >= 2) {
+      // ------------------------------------------------------------ rotate + quantize
+      // this rank's columns [c0, c1) of every row, from whole Hadamard blocks
+      const int c0 = s0 * 256, c1 = min(p.K, (s0 + n) * 256), U = p.block < 32 ? 32 : p.block;
+      const int u0 = c0 / U, u1 = (c1 + U - 1) / U, me = (int)threadIdx.x - 64;
+      uint16_t* rows = reinterpret_cast<uint16_t*>(smem + p.off_rows);
+      int32_t* rot = reinterpret_cast<int32_t*>(smem + p.off_rot);
+      const uint4* src = reinterpret_cast<const uint4*>(p.xb);
+      for (int i = me; i < p.T * p.K / 8; i += FUSED_WARPS * 32) reinterpret_cast<uint4*>(rows)[i] = __ldg(src + i);
+      for (int i = me; i < (u1 - u0) * U / 4; i += FUSED_WARPS * 32)
+        reinterpret_cast<int4*>(rot)[i] = __ldg(reinterpret_cast<const int4*>(p.rot + u0 * U) + i);
+      asm volatile("bar.sync 1, %0;" ::"n"(FUSED_WARPS * 32) : "memory");
+      const int nu = u1 - u0;
+      for (int j = warp - 2; j < nu * p.T; j += FUSED_WARPS) {
+        const int t = j / nu, u = u0 + j - t * nu;
+        mx_rotate_unit(rows + (size_t)t * p.K, rot + (u - u0) * U, u * U, p.block, p.inv_sqrt_b,
+                       [&](int k, uint8_t*& codes, uint8_t*& sf) {
+                         if (k < c0 || k >= c1) return false;
+                         const int c = k - c0, step = c >> 8, byte = (c & 255) >> 1;
+                         // 128-byte swizzle: 16-byte unit j of row t at unit j ^ (t % 8)
+                         codes = smem + p.off_x + step * PB + t * 128 + (((byte >> 4) ^ (t & 7)) << 4) + (byte & 15);
+                         sf = smem + p.off_x + n * PB + step * FUSED_SF + ((c & 255) >> 7) * 256 + t * 16 + ((c >> 5) & 3);
+                         return true;
+                       });
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(xready);
+    }
+  }
+  if (warp >= 4) {
     const int q = warp & 3;
     const bool ok = n > 0 && mbar_wait(accfull, 0, p.status, ST_TIMEOUT_MMA, abort_flag, p.wait_ns);
     if (ok) tc_fence_after();
@@ -445,18 +495,36 @@ cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int s
   static SmemLimit limit_once;
   cudaError_t e = limit_once.raise(reinterpret_cast<const void*>(mx_few_kernel<MODE>));
   if (e != cudaSuccess) return e;
-  // ranks per cluster: the fewest that give every SM a CTA, two steps each at least
+  // Ranks per cluster: as many as leave every CTA an SM, two steps each at
+  // least.  33 tiles of 32 steps: 12.7, 9.9, 8.4, 9.1 us with 1, 2, 4, 8 ranks.  The
+  // gate/up products split only while half the SMs are left, where the down
+  // products' CTAs start and fetch their weights early (64 tiles: 19.6 us for
+  // the layer with 1 rank, 21.2 with 2).
+  const int fill = MODE == GATE_UP ? sms / 2 : sms;
   int S = 1;
-  while (S < 8 && (int64_t)tiles * ny * S < sms && 4 * S <= steps) S *= 2;
-  const int stage = NA * (128 * 128 + 1024) + p.NT * 128 + 1024;
-  const int parts = (NA * p.NT * FEW_PITCH * 4 + 1023) & ~1023;   // the partial sums overlay the stages
-  // one CTA per SM: shared memory full of stages; more of them: two share an SM
-  const int limit = (int64_t)tiles * ny * S > sms ? 115712 : 230400;
-  p.stages = (limit - FEW_TAIL - 1024) / stage;
-  if (p.stages > FEW_MAX_STAGES) p.stages = FEW_MAX_STAGES;
+  while (S < 8 && (int64_t)tiles * ny * 2 * S <= fill && 4 * S <= steps) S *= 2;
+  const int stage = NA * (128 * 128 + 1024) + (MODE == FUSED ? 0 : p.NT * 128 + 1024);
   const int most = (steps + S - 1) / S;
+  // FUSED: the token codes and scales of every step, the rows, the table's entries
+  const int U = p.block < 32 ? 32 : p.block;
+  const int x_bytes = MODE == FUSED ? (most * (p.NT * 128 + FUSED_SF) + 256 + 1023) & ~1023 : 0;
+  const int rows_bytes = MODE == FUSED ? (p.T * p.K * 2 + 1023) & ~1023 : 0;
+  const int rot_bytes = MODE == FUSED ? ((most * 256 + 2 * U) * 4 + 1023) & ~1023 : 0;
+  const int fixed = x_bytes + rows_bytes + rot_bytes;
+  const int parts = (NA * p.NT * FEW_PITCH * 4 + 1023) & ~1023;   // the partial sums overlay the stages
+  // one CTA per SM, shared memory full of stages, if all are resident that way (a
+  // cluster's CTAs lie in one group of SMs: 148, 148, 132 and 120 for clusters of
+  // 1, 2, 4 and 8 on 148 SMs); otherwise two share an SM
+  const int64_t room = S <= 2 ? sms : S == 4 ? sms * 8 / 9 : sms * 4 / 5;
+  const int limit = (int64_t)tiles * ny * S > room ? 115712 : 230400;
+  p.stages = (limit - FEW_TAIL - 1024 - fixed) / stage;
+  if (p.stages < 1) return cudaErrorInvalidValue;
+  if (p.stages > FEW_MAX_STAGES) p.stages = FEW_MAX_STAGES;
   if (p.stages > most) p.stages = most < 1 ? 1 : most;
-  p.tail = p.stages * stage > parts ? p.stages * stage : parts;
+  p.off_x = p.stages * stage > parts ? p.stages * stage : parts;
+  p.off_rows = p.off_x + x_bytes;
+  p.off_rot = p.off_rows + rows_bytes;
+  p.tail = p.off_rot + rot_bytes;
   uint32_t cols = 32;
   while ((int)cols < NA * p.NT + p.stages * (NA + 1) * 8) cols *= 2;
   p.tmem_cols = cols;
@@ -501,6 +569,26 @@ cudaError_t launch_mx_few(const GemmLaunch& a, cudaStream_t st, const char** why
     return cudaErrorInvalidValue;
   }
   return launch_mode<LINEAR>(tm, p, (a.N + 127) / 128, 1, (a.K + 255) / 256, a.num_sms > 0 ? a.num_sms : 148, st);
+}
+
+// The rows of a few tokens fit beside the weights' stages, and every CTA has an
+// SM to itself; the redundant transform is a few thousand values per CTA.
+bool mx_layer_fused(int M, int N, int K, int sms) {
+  return M <= 4 && (int64_t)M * K <= 16384 && K <= 8192 && (N + 127) / 128 <= sms;
+}
+
+cudaError_t launch_mx_layer_fused(const GemmLaunch& a, const uint16_t* x, const int32_t* rot, int block, float inv_sqrt_b,
+                                  cudaStream_t st) {
+  FewMaps tm;
+  FewParams p{};
+  p.T = a.M; p.NT = token_columns(a.M); p.K = a.K; p.N = a.N;
+  p.w_sf = a.w_bscale;
+  p.xb = x; p.rot = rot; p.block = block; p.inv_sqrt_b = inv_sqrt_b;
+  p.Y = a.Y; p.out_fp32 = a.out_fp32;
+  p.status = a.status; p.wait_ns = a.wait_ns; p.inject_tx = a.inject_tx;
+  if (!mx_code_map(&tm.w, a.w_codes, a.N, a.K, 128)) return cudaErrorInvalidValue;
+  tm.x = tm.w;   // (not used)
+  return launch_mode<FUSED>(tm, p, (a.N + 127) / 128, 1, (a.K + 255) / 256, a.num_sms > 0 ? a.num_sms : 148, st);
 }
 
 cudaError_t launch_moe_products(const MoeLaunch& a, const uint8_t* xq, const uint8_t* xq_sf, uint8_t* hq, uint8_t* hq_sf,

@@ -409,7 +409,9 @@ def _workspace(n):
 @pytest.mark.parametrize("M,N,K,block", [(1, 256, 64, 64), (1, 515, 4096, 128), (3, 100, 192, 16), (8, 1000, 1344, 32),
                                          (16, 384, 2048, 1024), (17, 129, 1152, 128), (40, 300, 512, 512),
                                          (64, 256, 8192, 256), (65, 256, 256, 64), (200, 640, 1152, 128),
-                                         (2, 64, 16384, 512)])
+                                         (2, 64, 16384, 512), (4, 300, 4096, 1024), (2, 640, 8192, 512),
+                                         (1, 2305, 1024, 32), (3, 2048, 1344, 64), (1, 129, 8192, 1024),
+                                         (4, 4300, 256, 16), (1, 18900, 512, 256), (2, 4200, 1088, 64)])
 def test_layer(L, M, N, K, block):
     X, rot_t, wc, wsf, A, B = _layer_case(M, N, K, block)
     ws, st = _workspace(rq.rq_mxfp4_layer_workspace(M, N, K)), _status()
