@@ -59,9 +59,18 @@ __device__ __forceinline__ void mx_rotate_epl(const uint16_t* xs, const int32_t*
                                               const Sink& sink) {
   const int lane = threadIdx.x & 31, k0 = base + lane * EPL;
   float v[EPL];
+  int32_t tab[EPL];
+  if constexpr (EPL >= 4) {
+#pragma unroll
+    for (int i = 0; i < EPL; i += 4)
+      *reinterpret_cast<int4*>(tab + i) = *reinterpret_cast<const int4*>(rot + lane * EPL + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) tab[i] = rot[lane * EPL + i];
+  }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int32_t r = rot[lane * EPL + i];
+    const int32_t r = tab[i];
     v[i] = __uint_as_float(((uint32_t)xs[r & 0x7fffffff] << 16) ^ ((uint32_t)r & 0x80000000u));
   }
 #pragma unroll

@@ -134,10 +134,12 @@ __device__ __forceinline__ uint32_t few_idesc(int n, uint32_t id) {
 enum { LINEAR = 0, GATE_UP = 1, DOWN = 2, FUSED = 3 };
 constexpr int FUSED_SF = 512;           // FUSED: scale bytes per step, two tiles 256 bytes apart: the rows past
                                         // the 16th that a tile's copy also brings are other tiles', not used
-constexpr int FUSED_WARPS = 6;          // warps 2-7 transform the rows
+constexpr int FUSED_THREADS = 384;
+constexpr int FUSED_WARPS = FUSED_THREADS / 32 - 2;   // all but the first two transform the rows
+__host__ __device__ constexpr int few_threads(int mode) { return mode == FUSED ? FUSED_THREADS : FEW_THREADS; }
 
 template <int MODE>
-__global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_constant__ FewMaps tm,
+__global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __grid_constant__ FewMaps tm,
                                                                 const __grid_constant__ FewParams p) {
   constexpr int NA = MODE == GATE_UP ? 2 : 1;
   constexpr int PA = 128 * 128, SF = 1024;            // weight codes, scales of 128 rows per stage
@@ -154,7 +156,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
   uint64_t* accfull = empty + FEW_MAX_STAGES;
   uint64_t* mdrain = accfull + 1;
   uint64_t* xready = mdrain + 1;          // FUSED: the rows are quantized
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xready + 1);
+  uint64_t* xfull = xready + 1;           // FUSED: the rows and the table are here
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xfull + 1);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
   uint32_t* words = tmem_slot + 4;
   uint16_t* act = reinterpret_cast<uint16_t*>(words + 8);
@@ -174,6 +177,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
     mbar_init(accfull, 1);
     mbar_init(mdrain, 1);
     mbar_init(xready, FUSED_WARPS);
+    mbar_init(xfull, 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm.w);
@@ -238,6 +242,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
         bulk_g2s(s + NA * (PA + SF) + PB, p.x_sf + (size_t)a * KT * 512 + (size_t)q.kt * 1024, sfb, bar);
       }
     };
+    if (MODE == FUSED && one) {   // the rows, and the table's entries of this rank's columns (whole Hadamard blocks)
+      const int U = p.block < 32 ? 32 : p.block;
+      const int u0 = s0 * 256 / U, u1 = (min(p.K, (s0 + n) * 256) + U - 1) / U;
+      if (n > 0) {
+        mbar_expect_tx(xfull, (uint32_t)(p.T * p.K * 2 + (u1 - u0) * U * 4));
+        bulk_g2s(smem + p.off_rot, p.rot + u0 * U, (uint32_t)(u1 - u0) * U * 4, xfull);
+        bulk_g2s(smem + p.off_rows, p.xb, (uint32_t)(p.T * p.K * 2), xfull);
+      }
+    }
     Pos q{0, 0, s0 % spe, s0 / spe};
     int i = 0;
     if (p.early) {   // the first stages' weights now, their tokens once the previous kernel is done
@@ -253,12 +266,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
       load(q, i == 0, true, true);
       next(q);
     }
+    if (MODE == FUSED && n > 0 && *abort_flag) mbar_drain(xfull, 0, p.wait_ns);
     if (i < n)   // let the copies already issued land (bounded)
       for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j) mbar_drain(&full[j % p.stages], (j / p.stages) & 1, p.wait_ns);
   } else if (warp == 1) {
     if (n > 0) {
       const bool one = elect_one();
-      bool ok = true;
       int s = 0, ph = 0, kt = s0 % spe;
       // descriptors of the first stage; the address field counts 16-byte units,
       // so everything else is one addition (rebuilding them for every
@@ -266,11 +279,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
       const uint64_t d_op = smem_desc(sbase, 16, 1024, 2), d_sf = smem_desc(sbase + NA * PA + (MODE == FUSED ? 0 : PB), 16, 128, 0);
       const uint64_t d_x = smem_desc(sbase + (MODE == FUSED ? p.off_x : NA * PA), 16, 1024, 2);
       const uint64_t d_xsf = smem_desc(sbase + (MODE == FUSED ? p.off_x + n * PB : NA * PA + PB + NA * SF), 16, 128, 0);
-      if (MODE == FUSED) ok = warp_wait(xready, 0, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+      // No wait here hands out an answer: with a branch on one the compiler no
+      // longer takes what follows for warp-uniform.  After a wait has run out the
+      // others return at once and the loop runs to its end on whatever is there.
+      if (MODE == FUSED) mbar_wait(xready, 0, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
       const uint32_t id0 = few_idesc(p.NT, 0), id2 = few_idesc(p.NT, 2);
-      for (int i = 0; i < n && ok; ++i) {
-        ok = warp_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
-        if (!ok) break;
+      for (int i = 0; i < n; ++i) {
+        mbar_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
         tc_fence_after();
         const int sct = min(2, KT - kt * 2), kkn = min(4, p.K / 64 - kt * 4);
         const uint32_t st = (uint32_t)(s * STAGE) >> 4;
@@ -300,7 +315,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
         if (++s == p.stages) { s = 0; ph ^= 1; }
         if (++kt == spe) kt = 0;
       }
-      if (!ok) {   // wait (bounded) for the MMAs already issued
+      if (*abort_flag) {   // wait (bounded) for the MMAs issued
         if (one) tc_commit(mdrain);
         mbar_drain(mdrain, 0, p.wait_ns);
       }
@@ -333,15 +348,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
       // ------------------------------------------------------------ rotate + quantize
       // this rank's columns [c0, c1) of every row, from whole Hadamard blocks
       const int c0 = s0 * 256, c1 = min(p.K, (s0 + n) * 256), U = p.block < 32 ? 32 : p.block;
-      const int u0 = c0 / U, u1 = (c1 + U - 1) / U, me = (int)threadIdx.x - 64;
-      uint16_t* rows = reinterpret_cast<uint16_t*>(smem + p.off_rows);
-      int32_t* rot = reinterpret_cast<int32_t*>(smem + p.off_rot);
-      const uint4* src = reinterpret_cast<const uint4*>(p.xb);
-      for (int i = me; i < p.T * p.K / 8; i += FUSED_WARPS * 32) reinterpret_cast<uint4*>(rows)[i] = __ldg(src + i);
-      for (int i = me; i < (u1 - u0) * U / 4; i += FUSED_WARPS * 32)
-        reinterpret_cast<int4*>(rot)[i] = __ldg(reinterpret_cast<const int4*>(p.rot + u0 * U) + i);
-      asm volatile("bar.sync 1, %0;" ::"n"(FUSED_WARPS * 32) : "memory");
-      const int nu = u1 - u0;
+      const int u0 = c0 / U, u1 = (c1 + U - 1) / U;
+      const uint16_t* rows = reinterpret_cast<const uint16_t*>(smem + p.off_rows);
+      const int32_t* rot = reinterpret_cast<const int32_t*>(smem + p.off_rot);
+      const bool ok = n > 0 && mbar_wait(xfull, 0, p.status, ST_TIMEOUT_LOAD, abort_flag, p.wait_ns);
+      const int nu = ok ? u1 - u0 : 0;
+#pragma unroll 2
       for (int j = warp - 2; j < nu * p.T; j += FUSED_WARPS) {
         const int t = j / nu, u = u0 + j - t * nu;
         mx_rotate_unit(rows + (size_t)t * p.K, rot + (u - u0) * U, u * U, p.block, p.inv_sqrt_b,
@@ -359,7 +371,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
       if (lane == 0) mbar_arrive(xready);
     }
   }
-  if (warp >= 4) {
+  if (warp >= 4 && warp < 8) {
     const int q = warp & 3;
     const bool ok = n > 0 && mbar_wait(accfull, 0, p.status, ST_TIMEOUT_MMA, abort_flag, p.wait_ns);
     if (ok) tc_fence_after();
@@ -396,7 +408,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mx_few_kernel(const __grid_con
       }
       return v;
     };
-    for (int t = (int)rank + warp * (int)S; t < p.T; t += (int)S * (FEW_THREADS / 32)) {
+    for (int t = (int)rank + warp * (int)S; t < p.T; t += (int)S * (few_threads(MODE) / 32)) {
       if constexpr (MODE == GATE_UP) {
         if (!flag[t]) continue;
         float v[4];
@@ -500,7 +512,7 @@ cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int s
   // gate/up products split only while half the SMs are left, where the down
   // products' CTAs start and fetch their weights early (64 tiles: 19.6 us for
   // the layer with 1 rank, 21.2 with 2).
-  const int fill = MODE == GATE_UP ? sms / 2 : sms;
+  const int fill = MODE == GATE_UP ? sms / 2 : MODE == FUSED ? 2 * sms : sms;
   int S = 1;
   while (S < 8 && (int64_t)tiles * ny * 2 * S <= fill && 4 * S <= steps) S *= 2;
   const int stage = NA * (128 * 128 + 1024) + (MODE == FUSED ? 0 : p.NT * 128 + 1024);
@@ -543,7 +555,7 @@ cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int s
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * S), (unsigned)ny);
-  cfg.blockDim = dim3(FEW_THREADS);
+  cfg.blockDim = dim3(few_threads(MODE));
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cfg.attrs = attr;

@@ -151,13 +151,15 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
     if (rank == 0) {
       const bool one = elect_one();
       int s = 0, ph = 0, acc_ph = 1;
-      bool ok = true;
       // descriptors of the first stage; the address field counts 16-byte units
       const uint64_t d_op = smem_desc(sbase, 16, 1024, 2), d_sf = smem_desc(sbase + MG_PA + MG_PB, 16, 128, 0);
-      for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+      // No wait here hands out an answer: with a branch on one the compiler no
+      // longer takes what follows for warp-uniform.  After a wait has run out the
+      // others return at once, and the loop ends with its tile.
+      for (int tile = tile0; tile < ntiles; tile += tstep) {
+        if (uniform(*abort_flag)) break;
         for (int kt = 0; kt < nk; ++kt) {
-          ok = warp_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
-          if (!ok) break;
+          mbar_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
           tc_fence_after();
           const uint32_t st = (uint32_t)(s * MG_STAGE) >> 4;
           // the scales to the stage's own TMEM columns, free again when the stage is
@@ -172,8 +174,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
             }
           }
           if (kt == 0) {   // (the first tile finds the accumulator empty)
-            ok = warp_wait(accempty, acc_ph, p.status, ST_TIMEOUT_EPI, abort_flag, p.wait_ns);
-            if (!ok) break;
+            mbar_wait(accempty, acc_ph, p.status, ST_TIMEOUT_EPI, abort_flag, p.wait_ns);
             acc_ph ^= 1;
             tc_fence_after();
           }
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
           if (++s == MG_STAGES) { s = 0; ph ^= 1; }
         }
       }
-      if (!ok) {   // wait (bounded) for the MMAs already issued
+      if (*abort_flag) {   // wait (bounded) for the MMAs issued
         if (one) tc_commit2_mc(mdrain, 0x1);
         mbar_drain(mdrain, 0, p.wait_ns);
       }
