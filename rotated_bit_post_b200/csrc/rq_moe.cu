@@ -85,16 +85,15 @@ __global__ void __launch_bounds__(PREP_THREADS) __cluster_dims__(PREP_CLUSTER, 1
     for (int m = 16; m; m >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, m);
     if (lane == 0) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(home + e * 4), "f"(s0) : "memory");
   }
-  const auto sink = [&](int k, uint8_t*& codes, uint8_t*& sf) {
+  // rotated blocks, whole Hadamard blocks per warp and turn
+  const int nu = p.K / (p.block < 32 ? 32 : p.block);
+  const auto sink = [&](int, int k, uint8_t*& codes, uint8_t*& sf) {
     codes = p.xq + (size_t)t * (p.K / 2) + k / 2;
     sf = p.xq_sf + mx_sf_offset(t, k / 32, p.K);
     return true;
   };
-  // rotated blocks, `unit` coordinates (whole Hadamard blocks) per warp and turn
-  const int unit = p.block < 32 ? 32 : p.block;
-  for (int u = rank + warp * PREP_CLUSTER; u < p.K / unit; u += PREP_CLUSTER * (PREP_THREADS / 32)) {
-    mx_rotate_unit(xs, p.rot + u * unit, u * unit, p.block, p.inv_sqrt_b, sink);
-  }
+  mx_rotate_units(xs, 0, p.rot, 0, nu, nu, rank + warp * PREP_CLUSTER, PREP_CLUSTER * (PREP_THREADS / 32), p.block,
+                  p.inv_sqrt_b, sink);
   cluster_sync();
   if (rank != 0 || warp != 0) return;
   // ------------------------------------------------------------ the top_k experts

@@ -19,12 +19,14 @@ namespace rq {
 namespace {
 
 // ------------------------------------------------------------ rotate + quantize
-// Persistent over groups of R rows (1, 2, 4 or 8), two groups in flight: a group's
+// Persistent over groups of R rows (1, 2, 4 or 8), nbuf groups in flight: a group's
 // rows land in shared memory by bulk copies, at a pitch that puts the R rows
 // 128 / R bytes apart modulo the banks.  A warp's lanes are R rows x 32 / R
-// segments of 64 rotated coordinates; a thread gathers its segment through the
-// signed-permutation table (16 bits per coordinate: byte offset, sign in bit
-// 15), two chunks of 32 that are one MXFP4 block each.
+// segments of 64 rotated coordinates (a unit); a thread gathers its segment through
+// the signed-permutation table (16 bits per coordinate: byte offset, sign in bit
+// 15), two chunks of 32 that are one MXFP4 block each.  Units are dealt to the
+// warps round robin through the groups, without a barrier between them; the
+// last warp to leave a group refills its buffer.
 // Butterflies: strides 1 .. 16 inside the chunks, 32 between the two chunks,
 // 64 between the chunks after one of them was exchanged with the neighbouring
 // segment's (half the shuffles of a butterfly across lanes), 128 and up across
@@ -42,10 +44,11 @@ struct MxqParams {
   uint64_t wait_ns;
   uint32_t inject_tx;
   int rows, K, block, lr;   // lr: log2 of the rows per group
-  int ngroups;
+  int ngroups, nbuf;
   float isb;                // fp32(1 / sqrt(block))
 };
 
+constexpr int MXQ_MAXBUF = 8;
 constexpr int MXQ_SEG = 144;   // bytes of a segment's table entries: 64 x 2, and 16 that shift the banks
 
 // (p, q) of two values each -> (s p + q, p - s q), s = +-1
@@ -82,6 +85,18 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   float d;
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// eight values to eight E2M1 nibbles, the first in the low bits
+__device__ __forceinline__ uint32_t pack8(const float* v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
 }
 
 // 32 coordinates of one chunk through the table
@@ -142,14 +157,9 @@ __device__ __forceinline__ uint32_t quantize32(float (&v)[32], float isb, uint4&
   uint32_t w[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    w[j] = 0u;
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      float a = v[8 * j + e], b = v[8 * j + e + 1];
-      mul2(a, b, f);
-      w[j] |= (uint32_t)cvt_e2m1x2(b, a) << (4 * e);
-    }
-    if (sb == 255u) w[j] = 0u;
+    for (int e = 0; e < 8; e += 2) mul2(v[8 * j + e], v[8 * j + e + 1], f);
+    w[j] = sb == 255u ? 0u : pack8(v + 8 * j);
   }
   out = make_uint4(w[0], w[1], w[2], w[3]);
   return sb;
@@ -161,24 +171,29 @@ __global__ void __launch_bounds__(MXQ_THREADS, 1) mx_quantize_kernel(const __gri
   const int nseg = K / 64;
   const int pitch = 2 * K + (lr ? 128 >> lr : 0);
   uint8_t* tab = smem;
-  uint8_t* rowbuf = smem + nseg * MXQ_SEG;              // [2][R][pitch]
-  uint64_t* full = reinterpret_cast<uint64_t*>(rowbuf + 2 * R * pitch);
-  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(full + 2);
+  uint8_t* rowbuf = smem + nseg * MXQ_SEG;              // [nbuf][R][pitch]
+  uint64_t* full = reinterpret_cast<uint64_t*>(rowbuf + p.nbuf * R * pitch);
+  int* done = reinterpret_cast<int*>(full + MXQ_MAXBUF);   // warps that have left a buffer's group
+  int* fills = done + MXQ_MAXBUF;                          // groups that went into a buffer so far
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(fills + MXQ_MAXBUF);
   const int nthreads = blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = nthreads >> 5;
+  const int mine = ((int)p.ngroups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // this CTA's groups
 
-  auto issue = [&](int g, int buf) {
-    const int r0 = g << lr, nr = min(R, p.rows - r0);
-    mbar_expect_tx(&full[buf], (uint32_t)nr * 2 * K + (g == (int)blockIdx.x ? p.inject_tx : 0u));
+  auto issue = [&](int j) {   // this CTA's j-th group, into buffer j % nbuf
+    const int buf = j % p.nbuf, r0 = ((int)blockIdx.x + j * (int)gridDim.x) << lr, nr = min(R, p.rows - r0);
+    ++fills[buf];
+    mbar_expect_tx(&full[buf], (uint32_t)nr * 2 * K + (j == 0 ? p.inject_tx : 0u));
     for (int i = 0; i < nr; ++i)
       bulk_g2s(rowbuf + (buf * R + i) * pitch, p.x + (size_t)(r0 + i) * K, (uint32_t)(2 * K), &full[buf]);
   };
   if (threadIdx.x == 0) {
-    mbar_init(&full[0], 1);
-    mbar_init(&full[1], 1);
+    for (int i = 0; i < p.nbuf; ++i) {
+      mbar_init(&full[i], 1);
+      done[i] = fills[i] = 0;
+    }
     *abort_flag = 0;
     fence_mbar_init();
-    issue(blockIdx.x, 0);
-    if (blockIdx.x + gridDim.x < p.ngroups) issue(blockIdx.x + gridDim.x, 1);
+    for (int j = 0; j < min(mine, p.nbuf); ++j) issue(j);
     // the product that reads these codes may be scheduled: it waits for this
     // grid before it reads them
     griddep_launch_dependents();
@@ -194,11 +209,14 @@ __global__ void __launch_bounds__(MXQ_THREADS, 1) mx_quantize_kernel(const __gri
   const int spw = 32 >> lr;                              // segments per warp
   const int rl = lane & (R - 1), sl = lane >> lr;
   const int nunits = (nseg + spw - 1) / spw;
-  int it = 0;
-  for (int g = blockIdx.x; g < p.ngroups; g += gridDim.x, ++it) {
-    const int buf = it & 1, r0 = g << lr, nr = min(R, p.rows - r0);
-    const bool ok = mbar_wait(&full[buf], (it >> 1) & 1, p.status, ST_TIMEOUT_LOAD, abort_flag, p.wait_ns);
-    for (int u = warp; ok && u < nunits; u += nwarps) {
+  // Every warp walks through all groups in order, also one without a unit there:
+  // its answer from a buffer's barrier is then always that of the next phase.
+  int first = warp;   // this warp's first unit of the group
+  int buf = 0, ph = 0;
+  for (int j = 0; j < mine; ++j) {
+    if (!warp_wait(&full[buf], ph, p.status, ST_TIMEOUT_LOAD, abort_flag, p.wait_ns)) break;
+    const int r0 = ((int)blockIdx.x + j * (int)gridDim.x) << lr, nr = min(R, p.rows - r0);
+    for (int u = first; u < nunits; u += nwarps) {
       const int seg = u * spw + sl;
       const bool live = seg < nseg && rl < nr;
       const bool odd = p.block > 64 && (seg & 1);
@@ -251,55 +269,65 @@ __global__ void __launch_bounds__(MXQ_THREADS, 1) mx_quantize_kernel(const __gri
         }
       }
     }
-    __syncthreads();   // everyone has read this group's rows
-    if (*abort_flag) {
-      // let the copies in flight land (bounded) before the shared memory goes away
-      if (threadIdx.x == 0) {
-        mbar_drain(&full[buf], (it >> 1) & 1, p.wait_ns);
-        if (g + (int)gridDim.x < p.ngroups) mbar_drain(&full[buf ^ 1], ((it + 1) >> 1) & 1, p.wait_ns);
+    __syncwarp();
+    if (lane == 0) {
+      __threadfence_block();
+      if (atomicAdd(&done[buf], 1) == nwarps - 1) {
+        done[buf] = 0;
+        if (j + p.nbuf < mine) {
+          fence_proxy_async_smem();
+          issue(j + p.nbuf);
+        }
       }
-      break;
     }
-    if (threadIdx.x == 0 && g + 2 * (int)gridDim.x < p.ngroups) {
-      fence_proxy_async_smem();
-      issue(g + 2 * gridDim.x, buf);
-    }
+    first = (first - nunits) % nwarps;   // the deal goes on where this group ended
+    if (first < 0) first += nwarps;
+    if (++buf == p.nbuf) { buf = 0; ph ^= 1; }
   }
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0)   // let the copies in flight land (bounded) before the shared memory goes away
+    for (int i = 0; i < p.nbuf; ++i)
+      if (fills[i]) mbar_drain(&full[i], (fills[i] - 1) & 1, p.wait_ns);
 }
 
 // ----------------------------------------------------------------- dequantize
-// A thread per 8 codes: a 4-byte read, a scale byte, 8 values out; 2^tx threads
-// along a row.
+// A thread per block: 16 bytes of codes, a scale byte, 32 values out in whole
+// 32-byte sectors; 2^tx threads along a row.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes, const uint8_t* bscale, T* out,
                                                             int rows, int K, int tx) {
-  const int words = K / 8;
+  const int blocks = K / 32;
   const int x = threadIdx.x & ((1 << tx) - 1), y = threadIdx.x >> tx, per = 256 >> tx;
   for (int m = (int)blockIdx.x * per + y; m < rows; m += (int)gridDim.x * per) {
-    const uint32_t* c = reinterpret_cast<const uint32_t*>(codes) + (size_t)m * words;
+    const uint4* c = reinterpret_cast<const uint4*>(codes + (size_t)m * (K / 2));
     T* o = out + (size_t)m * K;
-#pragma unroll 4
-    for (int w = x; w < words; w += 1 << tx) {
-      const uint32_t q = __ldg(c + w);
-      const float s = mx_scale(__ldg(bscale + mx_sf_offset(m, w / 4, K)));
-      float v[8];
+#pragma unroll 2
+    for (int kb = x; kb < blocks; kb += 1 << tx) {
+      const uint4 q4 = __ldg(c + kb);
+      const float s = mx_scale(__ldg(bscale + mx_sf_offset(m, kb, K)));
+      const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
+      uint32_t w[32 * sizeof(T) / 4];
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
+      for (int e = 0; e < 32; e += 2) {
         uint32_t h;   // two E2M1 -> two FP16, exact
-        asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(q >> (4 * e)));
+        asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(q[e / 8] >> (4 * (e & 7))));
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        v[e] = f.x * s;
-        v[e + 1] = f.y * s;
+        if constexpr (sizeof(T) == 4) {
+          w[e] = __float_as_uint(f.x * s);
+          w[e + 1] = __float_as_uint(f.y * s);
+        } else {
+          const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * s, f.y * s);
+          w[e / 2] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
       }
-      if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<float4*>(o)[2 * w] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(o)[2 * w + 1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        __nv_bfloat162 h[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        reinterpret_cast<uint4*>(o)[w] = *reinterpret_cast<const uint4*>(h);
-      }
+      for (int i = 0; i < (int)sizeof(T); ++i) store32(reinterpret_cast<uint8_t*>(o + kb * 32) + 32 * i, w + 8 * i);
     }
   }
 }
@@ -346,36 +374,41 @@ cudaError_t launch_mx_quantize(const K1Launch& a, cudaStream_t st) {
   cudaError_t e = limit.raise(reinterpret_cast<const void*>(mx_quantize_kernel));
   if (e != cudaSuccess) return e;
   const int sms = a.num_sms > 0 ? a.num_sms : 148;
-  auto bytes = [&](int lr) { return a.K / 64 * MXQ_SEG + (2 << lr) * (2 * a.K + (lr ? 128 >> lr : 0)) + 64; };
+  const int table = a.K / 64 * MXQ_SEG;
+  auto group = [&](int lr) { return (2 * a.K + (lr ? 128 >> lr : 0)) << lr; };   // bytes of a group's rows
   // rows per group: as many as put their gathers on different banks (8 rows: 2.1
-  // expected cycles for 32 lanes, 4 rows: 2.6, one row: 3.5) while two CTAs share
-  // an SM, or else one; a Hadamard block has to lie in one warp (32 / R segments
-  // of 64), and few rows are spread over the SMs
+  // expected cycles for 32 lanes, 4 rows: 2.6, one row: 3.5); a Hadamard block has
+  // to lie in one warp (32 / R segments of 64), two groups in shared memory, and few
+  // rows are spread over the SMs
   int lr = a.block <= 256 ? 3 : a.block == 512 ? 2 : 1;
   while (lr > 0 && (a.rows >> lr) < sms) --lr;
-  if (bytes(lr) > 115000) {
-    int two = lr;
-    while (two > 1 && bytes(two) > 115000) --two;
-    if (two >= 2) lr = two;
-    else while (lr > 0 && bytes(lr) > 232000) --lr;
-  }
+  while (lr > 0 && table + 2 * group(lr) > 232000) --lr;
   MxqParams p{};
   p.x = a.x; p.rot = a.rot; p.codes = a.codes; p.sf = a.bscale;
   p.status = a.status; p.wait_ns = a.wait_ns; p.inject_tx = a.inject_tx;
   p.rows = a.rows; p.K = a.K; p.block = a.block; p.lr = lr; p.isb = a.inv_sqrt_b;
   p.ngroups = (a.rows + (1 << lr) - 1) >> lr;
   const int units = (a.K / 64 + (32 >> lr) - 1) / (32 >> lr);
-  const bool two = bytes(lr) <= 115000;
-  const int most = two ? 8 : 16, turns = (units + most - 1) / most;
-  const int warps = (units + turns - 1) / turns;   // an even share of a group's units each
-  const int grid = p.ngroups < sms * (two ? 2 : 1) ? p.ngroups : sms * (two ? 2 : 1);
-  mx_quantize_kernel<<<grid, warps * 32, bytes(lr), st>>>(p);
+  // two CTAs of 8 warps per SM if three groups fit half of its shared memory, else
+  // one of 16; fewer warps when the CTA has fewer units
+  const bool two = table + 3 * group(lr) <= 115000;
+  const int room = (two ? 115000 : 232000) - table;
+  p.nbuf = room / group(lr) < MXQ_MAXBUF ? room / group(lr) : MXQ_MAXBUF;
+  const int most = sms * (two ? 2 : 1), grid = p.ngroups < most ? p.ngroups : most;
+  const int turns = (p.ngroups + grid - 1) / grid;
+  if (p.nbuf > turns) p.nbuf = turns;
+  const int64_t all = (int64_t)units * turns;
+  // (warps without a unit help with the table)
+  const int want = all > 4 ? (int)(all < 16 ? all : 16) : 4, cap = two ? 8 : 16;
+  const int warps = want < cap ? want : cap;
+  const int smem = table + p.nbuf * group(lr) + MXQ_MAXBUF * 16 + 16;
+  mx_quantize_kernel<<<grid, warps * 32, smem, st>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_mx_dequantize(const MxDequantLaunch& a, cudaStream_t st) {
-  int tx = 3;   // the threads along a row: a power of two up to 256, near a quarter of its words
-  while (tx < 8 && (4 << tx) < a.K / 8) ++tx;
+  int tx = 1;   // the threads along a row: a power of two up to 256, at most its blocks
+  while (tx < 8 && (2 << tx) <= a.K / 32) ++tx;
   const int per = 256 >> tx;
   const int64_t blocks = ((int64_t)a.rows + per - 1) / per, most = (int64_t)(a.num_sms > 0 ? a.num_sms : 148) * 32;
   const int grid = (int)(blocks < most ? blocks : most);

@@ -50,12 +50,12 @@ __device__ __forceinline__ float e2m1_value(uint32_t n) {
 }
 
 // One warp transforms and quantizes 32 EPL rotated coordinates from `base` on, EPL
-// consecutive ones per lane, of the BF16 row xs (shared memory): butterflies in
-// ascending stride, inside the lane and then across lanes.  rot: the table's
-// entries from `base` on.  sink(k, codes, sf) says where coordinate k's packed
-// codes and its block's scale byte go, or false for nowhere.
+// consecutive ones per lane, of the BF16 row xs (shared memory), row number m:
+// butterflies in ascending stride, inside the lane and then across lanes.  rot: the
+// table's entries from `base` on.  sink(m, k, codes, sf) says where coordinate k's
+// packed codes and its block's scale byte go, or false for nowhere.
 template <int EPL, class Sink>
-__device__ __forceinline__ void mx_rotate_epl(const uint16_t* xs, const int32_t* rot, int base, int block, float isb,
+__device__ __forceinline__ void mx_rotate_epl(const uint16_t* xs, int m, const int32_t* rot, int base, int block, float isb,
                                               const Sink& sink) {
   const int lane = threadIdx.x & 31, k0 = base + lane * EPL;
   float v[EPL];
@@ -103,7 +103,7 @@ __device__ __forceinline__ void mx_rotate_epl(const uint16_t* xs, const int32_t*
   float up = 0.f;
   if constexpr (EPL == 1) up = __shfl_down_sync(0xffffffffu, __fmul_rn(v[0], inv), 1);
   uint8_t *dst, *sf;
-  if (!sink(k0, dst, sf)) return;
+  if (!sink(m, k0, dst, sf)) return;
   if constexpr (EPL == 1) {
     if (!(lane & 1)) *dst = sb == 255u ? (uint8_t)0 : cvt_e2m1x2(up, __fmul_rn(v[0], inv));
   } else {
@@ -121,16 +121,28 @@ __device__ __forceinline__ void mx_rotate_epl(const uint16_t* xs, const int32_t*
   }
   if (k0 % 32 == 0) *sf = (uint8_t)sb;
 }
-// The same for max(block, 32) coordinates, whole Hadamard blocks.
+// Units of max(block, 32) coordinates, whole Hadamard blocks: unit j of `all` is
+// coordinates (u0 + j % nu) U ... of row j / nu; this warp takes j = first, first +
+// stride, ..., two at a time so that one's latencies cover the other's.  rot: the
+// table's entries from u0 U on.
+template <int EPL, class Sink>
+__device__ __forceinline__ void mx_rotate_loop(const uint16_t* rows, int K, const int32_t* rot, int u0, int nu, int all,
+                                               int first, int stride, int block, float isb, const Sink& sink) {
+#pragma unroll 2
+  for (int j = first; j < all; j += stride) {
+    const int m = j / nu, u = j - m * nu;
+    mx_rotate_epl<EPL>(rows + (size_t)m * K, m, rot + u * 32 * EPL, (u0 + u) * 32 * EPL, block, isb, sink);
+  }
+}
 template <class Sink>
-__device__ __forceinline__ void mx_rotate_unit(const uint16_t* xs, const int32_t* rot, int base, int block, float isb,
-                                               const Sink& sink) {
-  if (block <= 32) mx_rotate_epl<1>(xs, rot, base, block, isb, sink);
-  else if (block == 64) mx_rotate_epl<2>(xs, rot, base, 64, isb, sink);
-  else if (block == 128) mx_rotate_epl<4>(xs, rot, base, 128, isb, sink);
-  else if (block == 256) mx_rotate_epl<8>(xs, rot, base, 256, isb, sink);
-  else if (block == 512) mx_rotate_epl<16>(xs, rot, base, 512, isb, sink);
-  else mx_rotate_epl<32>(xs, rot, base, 1024, isb, sink);
+__device__ __forceinline__ void mx_rotate_units(const uint16_t* rows, int K, const int32_t* rot, int u0, int nu, int all,
+                                                int first, int stride, int block, float isb, const Sink& sink) {
+  if (block <= 32) mx_rotate_loop<1>(rows, K, rot, u0, nu, all, first, stride, block, isb, sink);
+  else if (block == 64) mx_rotate_loop<2>(rows, K, rot, u0, nu, all, first, stride, 64, isb, sink);
+  else if (block == 128) mx_rotate_loop<4>(rows, K, rot, u0, nu, all, first, stride, 128, isb, sink);
+  else if (block == 256) mx_rotate_loop<8>(rows, K, rot, u0, nu, all, first, stride, 256, isb, sink);
+  else if (block == 512) mx_rotate_loop<16>(rows, K, rot, u0, nu, all, first, stride, 512, isb, sink);
+  else mx_rotate_loop<32>(rows, K, rot, u0, nu, all, first, stride, 1024, isb, sink);
 }
 
 }  // namespace rq

@@ -351,21 +351,17 @@ __global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __gr
       const int u0 = c0 / U, u1 = (c1 + U - 1) / U;
       const uint16_t* rows = reinterpret_cast<const uint16_t*>(smem + p.off_rows);
       const int32_t* rot = reinterpret_cast<const int32_t*>(smem + p.off_rot);
-      const bool ok = n > 0 && mbar_wait(xfull, 0, p.status, ST_TIMEOUT_LOAD, abort_flag, p.wait_ns);
+      const bool ok = n > 0 && warp_wait(xfull, 0, p.status, ST_TIMEOUT_LOAD, abort_flag, p.wait_ns);
       const int nu = ok ? u1 - u0 : 0;
-#pragma unroll 2
-      for (int j = warp - 2; j < nu * p.T; j += FUSED_WARPS) {
-        const int t = j / nu, u = u0 + j - t * nu;
-        mx_rotate_unit(rows + (size_t)t * p.K, rot + (u - u0) * U, u * U, p.block, p.inv_sqrt_b,
-                       [&](int k, uint8_t*& codes, uint8_t*& sf) {
-                         if (k < c0 || k >= c1) return false;
-                         const int c = k - c0, step = c >> 8, byte = (c & 255) >> 1;
-                         // 128-byte swizzle: 16-byte unit j of row t at unit j ^ (t % 8)
-                         codes = smem + p.off_x + step * PB + t * 128 + (((byte >> 4) ^ (t & 7)) << 4) + (byte & 15);
-                         sf = smem + p.off_x + n * PB + step * FUSED_SF + ((c & 255) >> 7) * 256 + t * 16 + ((c >> 5) & 3);
-                         return true;
-                       });
-      }
+      const auto sink = [&](int t, int k, uint8_t*& codes, uint8_t*& sf) {
+        if (k < c0 || k >= c1) return false;
+        const int c = k - c0, step = c >> 8, byte = (c & 255) >> 1;
+        // 128-byte swizzle: 16-byte unit j of row t at unit j ^ (t % 8)
+        codes = smem + p.off_x + step * PB + t * 128 + (((byte >> 4) ^ (t & 7)) << 4) + (byte & 15);
+        sf = smem + p.off_x + n * PB + step * FUSED_SF + ((c & 255) >> 7) * 256 + t * 16 + ((c >> 5) & 3);
+        return true;
+      };
+      mx_rotate_units(rows, p.K, rot, u0, nu, nu * p.T, warp - 2, FUSED_WARPS, p.block, p.inv_sqrt_b, sink);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(xready);
@@ -373,7 +369,7 @@ __global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __gr
   }
   if (warp >= 4 && warp < 8) {
     const int q = warp & 3;
-    const bool ok = n > 0 && mbar_wait(accfull, 0, p.status, ST_TIMEOUT_MMA, abort_flag, p.wait_ns);
+    const bool ok = n > 0 && warp_wait(accfull, 0, p.status, ST_TIMEOUT_MMA, abort_flag, p.wait_ns);
     if (ok) tc_fence_after();
     for (int c = 0; c < NA * p.NT; c += 16) {
       uint32_t v[16];

@@ -56,6 +56,79 @@ __device__ __forceinline__ uint32_t mg_idesc(uint32_t id) {
   return (id << 4) | (1u << 7) | (1u << 10) | (32u << 17) | (1u << 23) | (16u << 24) | (id << 29);
 }
 
+// 128 accumulator columns of this warp's 32 rows, from TMEM, as packed BF16; the
+// loads go out two at a time (the MMAs wait for this)
+__device__ __forceinline__ void mg_take(uint32_t acc, uint32_t (&w)[64]) {
+#pragma unroll
+  for (int ch = 0; ch < 4; ch += 2) {
+    uint32_t v[2][32];
+    tmem_ld32(acc + ch * 32, v[0]);
+    tmem_ld32(acc + ch * 32 + 32, v[1]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t* s = v[i / 16] + 2 * (i % 16);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(s[0]), __uint_as_float(s[1]));
+      w[ch * 16 + i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+}
+// ... to rows row0 .. row0 + 31, columns n0 .. of Y: through a 32 x 32 box in
+// shared memory and TMA stores, or element by element when a row of Y is not a
+// multiple of 16 bytes
+__device__ __forceinline__ void mg_store(const MgParams& p, const CUtensorMap* ymap, const uint32_t (&w)[64],
+                                         uint32_t box, int row0, int n0) {
+  const int lane = threadIdx.x & 31;
+  if (p.tma_store) {
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+      if (lane == 0) bulk_wait_group_read<0>();   // the last store has read the box
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)),
+                     "r"(w[ch * 16 + 4 * c]), "r"(w[ch * 16 + 4 * c + 1]), "r"(w[ch * 16 + 4 * c + 2]),
+                     "r"(w[ch * 16 + 4 * c + 3])
+                     : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        // rows >= M and columns >= N are clipped by the map; a box wholly outside is not stored
+        if (row0 < p.M && n0 + ch * 32 < p.N) tma_store_2d(ymap, box, n0 + ch * 32, row0);
+        bulk_commit_group();
+      }
+    }
+  } else if (row0 + lane < p.M) {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.Y) + (size_t)(row0 + lane) * p.N + n0;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+      const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+      if (n0 + 2 * i < p.N) out[2 * i] = h.x;
+      if (n0 + 2 * i + 1 < p.N) out[2 * i + 1] = h.y;
+    }
+  }
+}
+// FP32 output straight from TMEM
+__device__ __forceinline__ void mg_store_fp32(const MgParams& p, uint32_t acc, int row, int n0) {
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t v[32];
+    tmem_ld32(acc + ch * 32, v);
+    tmem_ld_wait();
+    const int n = n0 + ch * 32;
+    float* out = static_cast<float*>(p.Y) + (size_t)row * p.N + n;
+    if (row >= p.M) continue;
+    if (n + 32 <= p.N && (p.N & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(out + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (n + i < p.N) out[i] = __uint_as_float(v[i]);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_constant__ MgMaps tm,
                                                                 const __grid_constant__ MgParams p) {
   extern __shared__ uint8_t smem[];
@@ -204,80 +277,16 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
     bool ok = true;
     for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++tc) {
       const int row0 = tile / nN * 256 + (int)rank * 128 + q * 32, n0 = tile % nN * 256 + half * 128;
-      ok = mbar_wait(accfull, tc & 1, p.status, ST_TIMEOUT_MMA, abort_flag, p.wait_ns);
+      ok = warp_wait(accfull, tc & 1, p.status, ST_TIMEOUT_MMA, abort_flag, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
-      if (p.out_fp32) {
-        const int row = row0 + lane;
-#pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t v[32];
-          tmem_ld32(acc + ch * 32, v);
-          tmem_ld_wait();
-          float* out = static_cast<float*>(p.Y) + (size_t)row * p.N + n0 + ch * 32;
-          if (row < p.M) {
-            if (n0 + ch * 32 + 32 <= p.N && (p.N & 3) == 0) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<uint4*>(out + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (n0 + ch * 32 + i < p.N) out[i] = __uint_as_float(v[i]);
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(accempty, 0);
-        continue;
-      }
-      // BF16: the warp's 32 x 128 values into registers, two to a word, and the
-      // accumulator back to the MMAs
       uint32_t w[64];
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t v[32];
-        tmem_ld32(acc + ch * 32, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-          w[ch * 16 + i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-      }
+      if (p.out_fp32) mg_store_fp32(p, acc, row0 + lane, n0);
+      else mg_take(acc, w);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(accempty, 0);
-      if (p.tma_store) {
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          const uint32_t buf = stg;
-          if (lane == 0) bulk_wait_group_read<0>();   // the last store has read the box
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)),
-                         "r"(w[ch * 16 + 4 * c]), "r"(w[ch * 16 + 4 * c + 1]), "r"(w[ch * 16 + 4 * c + 2]),
-                         "r"(w[ch * 16 + 4 * c + 3])
-                         : "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            // rows >= M and columns >= N are clipped by the map; a box wholly outside is not stored
-            if (row0 < p.M && n0 + ch * 32 < p.N) tma_store_2d(&tm.y, buf, n0 + ch * 32, row0);
-            bulk_commit_group();
-          }
-        }
-      } else if (row0 + lane < p.M) {
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.Y) + (size_t)(row0 + lane) * p.N + n0;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-          if (n0 + 2 * i < p.N) out[2 * i] = h.x;
-          if (n0 + 2 * i + 1 < p.N) out[2 * i + 1] = h.y;
-        }
-      }
+      if (!p.out_fp32) mg_store(p, &tm.y, w, stg, row0, n0);
     }
     if (lane == 0) bulk_wait_group<0>();   // the staging boxes outlive their stores
   }

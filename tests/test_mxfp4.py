@@ -231,7 +231,8 @@ def _packed(values):
 @pytest.mark.parametrize("M,K,block", [(1, 64, 64), (1, 4096, 128), (3, 192, 16), (5, 320, 32), (130, 1152, 128),
                                        (33, 1344, 64), (17, 2048, 256), (9, 1536, 512), (7, 3072, 1024),
                                        (2, 16384, 128), (300, 12288, 256), (1000, 1536, 128), (4, 16384, 1024),
-                                       (129, 128, 16)])
+                                       (129, 128, 16), (20000, 128, 32), (9001, 192, 64), (3000, 1536, 128),
+                                       (5000, 512, 512), (2500, 4096, 1024), (1300, 16384, 256), (700, 5120, 1024)])
 def test_quantize_parity(L, M, K, block):
     bits = _rows(M, K)
     bits[M // 2, : K // 2] = 0
@@ -326,7 +327,8 @@ def test_dequantize(L, rows, K):
 SHAPES = [(1, 1, 64), (1, 128, 192), (2, 300, 4096), (7, 129, 1152), (8, 256, 320), (16, 1000, 2048), (17, 4100, 512),
           (33, 64, 1344), (64, 640, 1152), (65, 384, 1024), (128, 256, 256), (130, 1153, 320), (257, 515, 1152),
           (1, 77, 16384), (300, 260, 4160),
-          (2600, 2104, 192), (2600, 2101, 448), (5000, 1280, 1152)]
+          (2600, 2104, 192), (2600, 2101, 448), (5000, 1280, 1152), (20000, 400, 2048),
+          (300, 19000, 576)]
 
 
 @pytest.mark.gpu
