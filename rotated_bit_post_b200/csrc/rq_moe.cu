@@ -9,9 +9,9 @@
 // with the activation transform (here), the gate/up products with the hidden
 // rows' quantization, the down products with the sum (rq_mxfew.cu).
 //
-// Routing: a cluster of eight CTAs per token.  Every CTA stages the token's
-// row, takes an eighth of the experts' logits (a warp per expert, 16-byte
-// reads; FP32 sums) and an eighth of the rotated blocks; the logits meet in the
+// Routing: a cluster of up to eight CTAs per token.  Every CTA stages the
+// token's row, takes its share of the experts' logits (a warp per expert, 16-byte
+// reads; FP32 sums) and of the rotated blocks; the logits meet in the
 // first CTA's shared memory, where one warp picks the experts.  The split
 // keeps one token's pass over the router (E K 2 bytes) off a single SM.
 #include <cuda_bf16.h>
@@ -28,7 +28,6 @@ namespace rq {
 namespace {
 
 constexpr int PREP_THREADS = 256;
-constexpr int PREP_CLUSTER = 8;
 constexpr int MOE_EMAX = 256;
 
 struct PrepParams {
@@ -38,7 +37,7 @@ struct PrepParams {
   int32_t* idx;
   float* wts;
   uint8_t *xq, *xq_sf;   // T x K/2 codes, one row tile of scales
-  int T, K, E, top_k, renorm, block;
+  int T, K, E, top_k, renorm, block, cluster;
   float inv_sqrt_b;
 };
 
@@ -53,11 +52,10 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(PREP_THREADS) __cluster_dims__(PREP_CLUSTER, 1, 1)
-    moe_route_kernel(const __grid_constant__ PrepParams p) {
+__global__ void __launch_bounds__(PREP_THREADS) moe_route_kernel(const __grid_constant__ PrepParams p) {
   extern __shared__ __align__(16) uint16_t xs[];   // the token's row
   __shared__ float logit[MOE_EMAX];
-  const int rank = (int)cluster_ctarank(), t = blockIdx.x / PREP_CLUSTER;
+  const int C = p.cluster, rank = (int)blockIdx.x % C, t = blockIdx.x / C;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the gate/up kernel may be scheduled: it waits for this grid before it reads
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -69,7 +67,7 @@ __global__ void __launch_bounds__(PREP_THREADS) __cluster_dims__(PREP_CLUSTER, 1
   cluster_sync();
   uint32_t home;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(home) : "r"(smem_u32(logit)), "r"(0));
-  for (int e = rank + warp * PREP_CLUSTER; e < p.E; e += PREP_CLUSTER * (PREP_THREADS / 32)) {
+  for (int e = rank + warp * C; e < p.E; e += C * (PREP_THREADS / 32)) {
     const uint4* w = reinterpret_cast<const uint4*>(p.router + (size_t)e * p.K);
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll 8
@@ -86,13 +84,13 @@ __global__ void __launch_bounds__(PREP_THREADS) __cluster_dims__(PREP_CLUSTER, 1
     if (lane == 0) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(home + e * 4), "f"(s0) : "memory");
   }
   // rotated blocks, whole Hadamard blocks per warp and turn
-  const int nu = p.K / (p.block < 32 ? 32 : p.block);
+  const int nu = p.K / (p.block < 64 ? 64 : p.block);
   const auto sink = [&](int, int k, uint8_t*& codes, uint8_t*& sf) {
     codes = p.xq + (size_t)t * (p.K / 2) + k / 2;
     sf = p.xq_sf + mx_sf_offset(t, k / 32, p.K);
     return true;
   };
-  mx_rotate_units(xs, 0, p.rot, 0, nu, nu, rank + warp * PREP_CLUSTER, PREP_CLUSTER * (PREP_THREADS / 32), p.block,
+  mx_rotate_units(xs, 0, p.rot, 0, nu, nu, rank + warp * C, C * (PREP_THREADS / 32), p.block,
                   p.inv_sqrt_b, sink);
   cluster_sync();
   if (rank != 0 || warp != 0) return;
@@ -157,8 +155,22 @@ cudaError_t launch_moe(const MoeLaunch& a, cudaStream_t st) {
   p.xq = xq; p.xq_sf = xq_sf;
   p.T = a.T; p.K = a.K; p.E = a.E; p.top_k = a.top_k; p.renorm = a.renorm; p.block = a.block;
   p.inv_sqrt_b = a.inv_sqrt_b;
-  moe_route_kernel<<<a.T * PREP_CLUSTER, PREP_THREADS, (size_t)a.K * 2, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  // CTAs per token: eight while they all fit the GPU twice
+  p.cluster = 8;
+  while (p.cluster > 1 && a.T * p.cluster > 2 * (a.num_sms > 0 ? a.num_sms : 148)) p.cluster /= 2;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.T * p.cluster));
+  cfg.blockDim = dim3(PREP_THREADS);
+  cfg.dynamicSmemBytes = (size_t)a.K * 2;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_route_kernel, p);
   if (e != cudaSuccess) return e;
   return launch_moe_products(a, xq, xq_sf, hq, hq_sf, active, st);
 }

@@ -74,7 +74,7 @@ __device__ __forceinline__ void mx_rotate_epl(const uint16_t* xs, int m, const i
     v[i] = __uint_as_float(((uint32_t)xs[r & 0x7fffffff] << 16) ^ ((uint32_t)r & 0x80000000u));
   }
 #pragma unroll
-  for (int h = 1; h < EPL; h <<= 1) {   // EPL <= block unless it is 1
+  for (int h = 1; h < EPL; h <<= 1) {   // (EPL <= block)
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (!(i & h)) {
@@ -100,28 +100,22 @@ __device__ __forceinline__ void mx_rotate_epl(const uint16_t* xs, int m, const i
   for (int s = 1; s < 32 / EPL; s <<= 1) am = fmax_nan(am, __shfl_xor_sync(0xffffffffu, am, s));
   const uint32_t sb = mx_scale_byte(am);
   const float inv = mx_inv_scale(sb);
-  float up = 0.f;
-  if constexpr (EPL == 1) up = __shfl_down_sync(0xffffffffu, __fmul_rn(v[0], inv), 1);
   uint8_t *dst, *sf;
   if (!sink(m, k0, dst, sf)) return;
-  if constexpr (EPL == 1) {
-    if (!(lane & 1)) *dst = sb == 255u ? (uint8_t)0 : cvt_e2m1x2(up, __fmul_rn(v[0], inv));
-  } else {
-    uint32_t w[(EPL + 7) / 8];
+  uint32_t w[(EPL + 7) / 8];
 #pragma unroll
-    for (int i = 0; i < (EPL + 7) / 8; ++i) w[i] = 0u;
+  for (int i = 0; i < (EPL + 7) / 8; ++i) w[i] = 0u;
 #pragma unroll
-    for (int i = 0; i < EPL; i += 2)
-      w[i / 8] |= (sb == 255u ? 0u : (uint32_t)cvt_e2m1x2(__fmul_rn(v[i + 1], inv), __fmul_rn(v[i], inv))) << (4 * (i & 7));
-    if constexpr (EPL == 2) *dst = (uint8_t)w[0];
-    else if constexpr (EPL == 4) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w[0];
-    else if constexpr (EPL == 8) *reinterpret_cast<uint32_t*>(dst) = w[0];
-    else if constexpr (EPL == 16) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  for (int i = 0; i < EPL; i += 2)
+    w[i / 8] |= (sb == 255u ? 0u : (uint32_t)cvt_e2m1x2(__fmul_rn(v[i + 1], inv), __fmul_rn(v[i], inv))) << (4 * (i & 7));
+  if constexpr (EPL == 2) *dst = (uint8_t)w[0];
+  else if constexpr (EPL == 4) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w[0];
+  else if constexpr (EPL == 8) *reinterpret_cast<uint32_t*>(dst) = w[0];
+  else if constexpr (EPL == 16) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   if (k0 % 32 == 0) *sf = (uint8_t)sb;
 }
-// Units of max(block, 32) coordinates, whole Hadamard blocks: unit j of `all` is
+// Units of max(block, 64) coordinates, whole Hadamard blocks: unit j of `all` is
 // coordinates (u0 + j % nu) U ... of row j / nu; this warp takes j = first, first +
 // stride, ..., two at a time so that one's latencies cover the other's.  rot: the
 // table's entries from u0 U on.
@@ -137,8 +131,7 @@ __device__ __forceinline__ void mx_rotate_loop(const uint16_t* rows, int K, cons
 template <class Sink>
 __device__ __forceinline__ void mx_rotate_units(const uint16_t* rows, int K, const int32_t* rot, int u0, int nu, int all,
                                                 int first, int stride, int block, float isb, const Sink& sink) {
-  if (block <= 32) mx_rotate_loop<1>(rows, K, rot, u0, nu, all, first, stride, block, isb, sink);
-  else if (block == 64) mx_rotate_loop<2>(rows, K, rot, u0, nu, all, first, stride, 64, isb, sink);
+  if (block <= 64) mx_rotate_loop<2>(rows, K, rot, u0, nu, all, first, stride, block, isb, sink);
   else if (block == 128) mx_rotate_loop<4>(rows, K, rot, u0, nu, all, first, stride, 128, isb, sink);
   else if (block == 256) mx_rotate_loop<8>(rows, K, rot, u0, nu, all, first, stride, 256, isb, sink);
   else if (block == 512) mx_rotate_loop<16>(rows, K, rot, u0, nu, all, first, stride, 512, isb, sink);

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __gr
       }
     };
     if (MODE == FUSED && one) {   // the rows, and the table's entries of this rank's columns (whole Hadamard blocks)
-      const int U = p.block < 32 ? 32 : p.block;
+      const int U = p.block < 64 ? 64 : p.block;
       const int u0 = s0 * 256 / U, u1 = (min(p.K, (s0 + n) * 256) + U - 1) / U;
       if (n > 0) {
         mbar_expect_tx(xfull, (uint32_t)(p.T * p.K * 2 + (u1 - u0) * U * 4));
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __gr
     if (warp >= 2) {
       // ------------------------------------------------------------ rotate + quantize
       // this rank's columns [c0, c1) of every row, from whole Hadamard blocks
-      const int c0 = s0 * 256, c1 = min(p.K, (s0 + n) * 256), U = p.block < 32 ? 32 : p.block;
+      const int c0 = s0 * 256, c1 = min(p.K, (s0 + n) * 256), U = p.block < 64 ? 64 : p.block;
       const int u0 = c0 / U, u1 = (c1 + U - 1) / U;
       const uint16_t* rows = reinterpret_cast<const uint16_t*>(smem + p.off_rows);
       const int32_t* rot = reinterpret_cast<const int32_t*>(smem + p.off_rot);
@@ -514,7 +514,7 @@ cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int s
   const int stage = NA * (128 * 128 + 1024) + (MODE == FUSED ? 0 : p.NT * 128 + 1024);
   const int most = (steps + S - 1) / S;
   // FUSED: the token codes and scales of every step, the rows, the table's entries
-  const int U = p.block < 32 ? 32 : p.block;
+  const int U = p.block < 64 ? 64 : p.block;
   const int x_bytes = MODE == FUSED ? (most * (p.NT * 128 + FUSED_SF) + 256 + 1023) & ~1023 : 0;
   const int rows_bytes = MODE == FUSED ? (p.T * p.K * 2 + 1023) & ~1023 : 0;
   const int rot_bytes = MODE == FUSED ? ((most * 256 + 2 * U) * 4 + 1023) & ~1023 : 0;
@@ -542,6 +542,8 @@ cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int s
   int smem = p.tail + FEW_TAIL + 1024;
   const int share = (int)cols * 456 - 1024;
   if (smem < share) smem = share;
+  // nor, in a cluster, for a neighbour that takes all of TMEM and half of shared memory
+  if (S > 1 && smem < 115712) smem = 115712;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -73,58 +73,84 @@ __device__ __forceinline__ void mg_take(uint32_t acc, uint32_t (&w)[64]) {
     }
   }
 }
-// ... to rows row0 .. row0 + 31, columns n0 .. of Y: through a 32 x 32 box in
-// shared memory and TMA stores, or element by element when a row of Y is not a
-// multiple of 16 bytes
-__device__ __forceinline__ void mg_store(const MgParams& p, const CUtensorMap* ymap, const uint32_t (&w)[64],
-                                         uint32_t box, int row0, int n0) {
+// ... to rows row0 .. row0 + 31, columns n0 .. n0 + 127 of Y by TMA stores of 32 x
+// 32 boxes in shared memory
+__device__ __forceinline__ void mg_store_tma(const MgParams& p, const CUtensorMap* ymap, const uint32_t (&w)[64],
+                                             uint8_t* box, int row0, int n0) {
   const int lane = threadIdx.x & 31;
-  if (p.tma_store) {
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
-      if (lane == 0) bulk_wait_group_read<0>();   // the last store has read the box
-      __syncwarp();
+  for (int ch = 0; ch < 4; ++ch) {
+    const int n = n0 + ch * 32;
+    if (lane == 0) bulk_wait_group_read<0>();   // the last store has read the box
+    __syncwarp();
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)),
-                     "r"(w[ch * 16 + 4 * c]), "r"(w[ch * 16 + 4 * c + 1]), "r"(w[ch * 16 + 4 * c + 2]),
-                     "r"(w[ch * 16 + 4 * c + 3])
-                     : "memory");
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        // rows >= M and columns >= N are clipped by the map; a box wholly outside is not stored
-        if (row0 < p.M && n0 + ch * 32 < p.N) tma_store_2d(ymap, box, n0 + ch * 32, row0);
-        bulk_commit_group();
-      }
-    }
-  } else if (row0 + lane < p.M) {
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.Y) + (size_t)(row0 + lane) * p.N + n0;
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-      if (n0 + 2 * i < p.N) out[2 * i] = h.x;
-      if (n0 + 2 * i + 1 < p.N) out[2 * i + 1] = h.y;
+    for (int c = 0; c < 4; ++c)   // 64-byte swizzle: 16-byte unit c of row r at unit c ^ (r / 2 % 4)
+      *reinterpret_cast<uint4*>(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+          make_uint4(w[ch * 16 + 4 * c], w[ch * 16 + 4 * c + 1], w[ch * 16 + 4 * c + 2], w[ch * 16 + 4 * c + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      // rows >= M and columns >= N are clipped by the map; a box wholly outside is not stored
+      if (row0 < p.M && n < p.N) tma_store_2d(ymap, smem_u32(box), n, row0);
+      bulk_commit_group();
     }
   }
 }
-// FP32 output straight from TMEM
-__device__ __forceinline__ void mg_store_fp32(const MgParams& p, uint32_t acc, int row, int n0) {
+// ... when a row of Y is not a multiple of 16 bytes: through the box too, row by row
+// with the lanes along it, two rows at a time for even N.  (Whole 16-byte units of
+// Y, shifted into place, measured slower: 178 us against 149 at 6240 x 5120 x 9972,
+// 145 against 149 at 15063 x 384 x 4511.)
+__device__ __forceinline__ void mg_store_ragged(const MgParams& p, const uint32_t (&w)[64], uint8_t* box, int row0, int n0) {
+  const int lane = threadIdx.x & 31, rows = min(32, p.M - row0);
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    const int n = n0 + ch * 32;
+    __syncwarp();   // (the box has been read)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)   // 16-byte unit c of row r at unit c ^ (r / 2 % 4)
+      *reinterpret_cast<uint4*>(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+          make_uint4(w[ch * 16 + 4 * c], w[ch * 16 + 4 * c + 1], w[ch * 16 + 4 * c + 2], w[ch * 16 + 4 * c + 3]);
+    __syncwarp();
+    uint16_t* out = static_cast<uint16_t*>(p.Y) + (size_t)row0 * p.N + n;
+    if ((p.N & 1) == 0) {
+      const int c = (lane & 15) * 2;   // (N even: n + c < N covers c + 1)
+#pragma unroll 8
+      for (int r = lane >> 4; r < rows; r += 2) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(box + r * 64 + (((c >> 3) ^ ((r >> 1) & 3)) << 4) + (c & 7) * 2);
+        if (n + c < p.N) *reinterpret_cast<uint32_t*>(out + (size_t)r * p.N + c) = v;
+      }
+    } else {
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r) {
+        const uint16_t v = *reinterpret_cast<const uint16_t*>(box + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+        if (n + lane < p.N) out[(size_t)r * p.N + lane] = v;
+      }
+    }
+  }
+}
+// FP32 output: 16 columns at a time through the box, half a warp along a row
+__device__ __forceinline__ void mg_store_fp32(const MgParams& p, uint32_t acc, uint8_t* box, int row0, int n0) {
+  const int lane = threadIdx.x & 31, c = lane & 15, rows = min(32, p.M - row0);
 #pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
     uint32_t v[32];
     tmem_ld32(acc + ch * 32, v);
     tmem_ld_wait();
-    const int n = n0 + ch * 32;
-    float* out = static_cast<float*>(p.Y) + (size_t)row * p.N + n;
-    if (row >= p.M) continue;
-    if (n + 32 <= p.N && (p.N & 3) == 0) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(out + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else {
+    for (int h = 0; h < 2; ++h) {
+      const int n = n0 + ch * 32 + h * 16;
+      __syncwarp();   // (the box has been read)
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (n + i < p.N) out[i] = __uint_as_float(v[i]);
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(v[h * 16 + 4 * q], v[h * 16 + 4 * q + 1], v[h * 16 + 4 * q + 2], v[h * 16 + 4 * q + 3]);
+      __syncwarp();
+      float* out = static_cast<float*>(p.Y) + (size_t)row0 * p.N + n;
+#pragma unroll 4
+      for (int r = lane >> 4; r < rows; r += 2) {
+        const float y = *reinterpret_cast<const float*>(box + r * 64 + (((c >> 2) ^ ((r >> 1) & 3)) << 4) + (c & 3) * 4);
+        if (n + c < p.N) out[(size_t)r * p.N + c] = y;
+      }
     }
   }
 }
@@ -272,7 +298,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
-    const uint32_t stg = sbase + MG_OFF_STG + (warp - 4) * MG_STG;
+    uint8_t* stg = smem + MG_OFF_STG + (warp - 4) * MG_STG;
     int tc = 0;
     bool ok = true;
     for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++tc) {
@@ -281,12 +307,13 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
       if (!ok) break;
       tc_fence_after();
       uint32_t w[64];
-      if (p.out_fp32) mg_store_fp32(p, acc, row0 + lane, n0);
+      if (p.out_fp32) mg_store_fp32(p, acc, stg, row0, n0);
       else mg_take(acc, w);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(accempty, 0);
-      if (!p.out_fp32) mg_store(p, &tm.y, w, stg, row0, n0);
+      if (p.tma_store) mg_store_tma(p, &tm.y, w, stg, row0, n0);
+      else if (!p.out_fp32) mg_store_ragged(p, w, stg, row0, n0);
     }
     if (lane == 0) bulk_wait_group<0>();   // the staging boxes outlive their stores
   }
