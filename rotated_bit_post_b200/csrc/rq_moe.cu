@@ -67,21 +67,36 @@ __global__ void __launch_bounds__(PREP_THREADS) moe_route_kernel(const __grid_co
   cluster_sync();
   uint32_t home;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(home) : "r"(smem_u32(logit)), "r"(0));
-  for (int e = rank + warp * C; e < p.E; e += C * (PREP_THREADS / 32)) {
-    const uint4* w = reinterpret_cast<const uint4*>(p.router + (size_t)e * p.K);
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll 8
+  // two experts per warp and turn: twice the reads in flight
+  const int stride = C * (PREP_THREADS / 32);
+  for (int e = rank + warp * C; e < p.E; e += 2 * stride) {
+    const bool two = e + stride < p.E;
+    const uint4* w0 = reinterpret_cast<const uint4*>(p.router + (size_t)e * p.K);
+    const uint4* w1 = reinterpret_cast<const uint4*>(p.router + (size_t)(two ? e + stride : e) * p.K);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int i = lane; i < chunks; i += 32) {
-      const uint4 a = __ldg(w + i), b = reinterpret_cast<const uint4*>(xs)[i];
-      s0 = fmaf(bf_lo(a.x), bf_lo(b.x), s0); s1 = fmaf(bf_hi(a.x), bf_hi(b.x), s1);
-      s0 = fmaf(bf_lo(a.y), bf_lo(b.y), s0); s1 = fmaf(bf_hi(a.y), bf_hi(b.y), s1);
-      s0 = fmaf(bf_lo(a.z), bf_lo(b.z), s0); s1 = fmaf(bf_hi(a.z), bf_hi(b.z), s1);
-      s0 = fmaf(bf_lo(a.w), bf_lo(b.w), s0); s1 = fmaf(bf_hi(a.w), bf_hi(b.w), s1);
-    }
-    s0 += s1;
+      const uint4 a = __ldg(w0 + i), c = __ldg(w1 + i), b = reinterpret_cast<const uint4*>(xs)[i];
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w}, cw[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int m = 16; m; m >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, m);
-    if (lane == 0) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(home + e * 4), "f"(s0) : "memory");
+      for (int q = 0; q < 4; ++q) {
+        s[0] = fmaf(bf_lo(aw[q]), bf_lo(bw[q]), s[0]);
+        s[1] = fmaf(bf_hi(aw[q]), bf_hi(bw[q]), s[1]);
+        s[2] = fmaf(bf_lo(cw[q]), bf_lo(bw[q]), s[2]);
+        s[3] = fmaf(bf_hi(cw[q]), bf_hi(bw[q]), s[3]);
+      }
+    }
+    s[0] += s[1];
+    s[2] += s[3];
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+      s[0] += __shfl_xor_sync(0xffffffffu, s[0], m);
+      s[2] += __shfl_xor_sync(0xffffffffu, s[2], m);
+    }
+    if (lane == 0) {
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(home + e * 4), "f"(s[0]) : "memory");
+      if (two) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(home + (e + stride) * 4), "f"(s[2]) : "memory");
+    }
   }
   // rotated blocks, whole Hadamard blocks per warp and turn
   const int nu = p.K / (p.block < 64 ? 64 : p.block);
