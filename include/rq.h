@@ -394,6 +394,7 @@ rq_status rq_mxfp4_dequantize(int32_t rows, int32_t K, const uint8_t* codes, con
  *   [device, N x K/2], w_bscale from rq_quantize_weights(RQ_MXFP4, ...);
  *   Y [device, M x N] FP32 or BF16 (out_fp32).  M >= 0, K % 64 == 0,
  *   K <= 16384.
+ *   At most 4 tokens with M K <= 16384 and K <= 8192 run in one launch.
  *   workspace [device] at least rq_mxfp4_layer_workspace(M, N, K) bytes, its
  *   contents undefined before and after; calls that may overlap on the GPU
  *   need one each.  That function returns -1 for a shape outside the limits.
@@ -420,8 +421,9 @@ rq_status rq_mxfp4_layer(int32_t M, int32_t N, int32_t K, int32_t block, const u
  *   rot, block: the rotation that W1's rows were quantized with.
  *   w1_codes [device, E x 2I x K/2]: gate rows 0..I-1, up rows I..2I-1;
  *   w1_bscale: E scale buffers of 2I rows each, one after another.
- *   w2_codes [device, E x K x I/2], w2_bscale: E scale buffers of K rows, their
- *   columns rotated with the plain block Hadamard of block2 channels (16, 32,
+ *   w2_codes [device, E x K x I/2], w2_bscale: E scale buffers of K rows (one
+ *   rq_quantize_weights call over all experts' rows gives both; w2 with K % 128
+ *   != 0 takes one call per expert), their columns rotated with the plain block Hadamard of block2 channels (16, 32,
  *   64 or 128).  A table with signs and a permutation is folded into W1
  *   instead: give channel i of the gate row perm[i] and of the up row perm[i]
  *   times its sign.
@@ -430,7 +432,9 @@ rq_status rq_mxfp4_layer(int32_t M, int32_t N, int32_t K, int32_t block, const u
  *   out; Y [device, T x K] FP32 or BF16 (out_fp32).
  *   workspace as rq_mxfp4_layer, rq_mxfp4_moe_workspace(...) bytes.
  * A NaN logit ranks as -infinity: the chosen experts are always top_k
- * different ones, and a token's NaN stays in its own row of Y.
+ * different ones, and a token's NaN stays in its own row of Y.  The weights are
+ * finite: a block of scale 255 in an expert that some token chose makes its
+ * rows of Y's columns NaN for every token of the call.
  */
 #define RQ_MOE_MAX_TOKENS 64
 #define RQ_MOE_MAX_EXPERTS 256

@@ -282,10 +282,10 @@ __global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __gr
       // No wait here hands out an answer: with a branch on one the compiler no
       // longer takes what follows for warp-uniform.  After a wait has run out the
       // others return at once and the loop runs to its end on whatever is there.
-      if (MODE == FUSED) mbar_wait(xready, 0, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+      if (MODE == FUSED) mbar_wait_soon(xready, 0, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
       const uint32_t id0 = few_idesc(p.NT, 0), id2 = few_idesc(p.NT, 2);
       for (int i = 0; i < n; ++i) {
-        mbar_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+        mbar_wait_soon(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
         tc_fence_after();
         const int sct = min(2, KT - kt * 2), kkn = min(4, p.K / 64 - kt * 4);
         const uint32_t st = (uint32_t)(s * STAGE) >> 4;

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
                                                                 const __grid_constant__ MgParams p) {
   extern __shared__ uint8_t smem[];
   if (smem_u32(smem) & 1023u) {   // (both CTAs see the same base)
-    if (threadIdx.x == 0) atomicCAS(p.status, 0, ST_SMEM_ALIGN);
+    if (threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, ST_SMEM_ALIGN);
     return;
   }
   const uint32_t sbase = smem_u32(smem);
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
       for (int tile = tile0; tile < ntiles; tile += tstep) {
         if (uniform(*abort_flag)) break;
         for (int kt = 0; kt < nk; ++kt) {
-          mbar_wait(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+          mbar_wait_soon(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
           tc_fence_after();
           const uint32_t st = (uint32_t)(s * MG_STAGE) >> 4;
           // the scales to the stage's own TMEM columns, free again when the stage is
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
             }
           }
           if (kt == 0) {   // (the first tile finds the accumulator empty)
-            mbar_wait(accempty, acc_ph, p.status, ST_TIMEOUT_EPI, abort_flag, p.wait_ns);
+            mbar_wait_soon(accempty, acc_ph, p.status, ST_TIMEOUT_EPI, abort_flag, p.wait_ns);
             acc_ph ^= 1;
             tc_fence_after();
           }

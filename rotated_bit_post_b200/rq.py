@@ -239,6 +239,15 @@ def rq_w4a4_linear2(M, N, K, a_codes, a_scale, a_zero_point, w_codes, w_scale, w
         _dev(Y), int(out_fp32), _dev(status), _stream(stream)))
 
 
+def _here(*tensors):
+    """The tensors lie on the current device, whose stream and kernels the call takes."""
+    import torch
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    for t in tensors:
+        if t.get_device() not in (here, -1):   # (_dev refuses host tensors)
+            raise ValueError(f"tensor on device {t.get_device()}, the current device is {here}")
+
+
 def _shape(what, t, elem_bytes, n):
     """The buffer holds at least n elements of that many bytes."""
     if t.element_size() != elem_bytes or t.numel() < n:
@@ -249,6 +258,7 @@ def _shape(what, t, elem_bytes, n):
 def rq_mxfp4_dequantize(codes, block_scale, out, out_fp32, stream=None):
     """Values of MXFP4 codes [rows, K/2] -> out [rows, K], FP32 or BF16."""
     rows, K = codes.shape[0], codes.shape[1] * 2
+    _here(codes, block_scale, out)
     _shape("block_scale", block_scale, 1, mx_sf_bytes(rows, K))
     _shape("out", out, 4 if out_fp32 else 2, rows * K)
     _check("rq_mxfp4_dequantize", lib().rq_mxfp4_dequantize(
@@ -264,6 +274,8 @@ def rq_mxfp4_layer(X, block, rot, w_codes, w_bscale, workspace, Y, out_fp32, sta
     """Y = Q(R X) W^T from BF16 rows, MXFP4 on both sides."""
     M, K = X.shape
     N = w_codes.shape[0]
+    _here(X, rot, w_codes, w_bscale, workspace, Y, status)
+    _shape("X", X, 2, M * K)
     _shape("rot", rot, 4, K)
     _shape("w_codes", w_codes, 1, N * (K // 2))
     _shape("w_bscale", w_bscale, 1, mx_sf_bytes(N, K))
@@ -284,6 +296,8 @@ def rq_mxfp4_moe(X, router, top_k, renorm, block, rot, w1_codes, w1_bscale, bloc
     rows), w2_codes [E, K, I/2]; routing out to topk_idx / topk_weight."""
     T, K = X.shape
     E, I = w1_codes.shape[0], w1_codes.shape[1] // 2
+    _here(X, router, rot, w1_codes, w1_bscale, w2_codes, w2_bscale, topk_idx, topk_weight, workspace, Y, status)
+    _shape("X", X, 2, T * K)
     _shape("router", router, 2, E * K)
     _shape("rot", rot, 4, K)
     _shape("w1_codes", w1_codes, 1, E * 2 * I * (K // 2))

@@ -154,6 +154,16 @@ def test_binding_checks_sizes(L):
         rq.rq_mxfp4_dequantize(c, s, torch.zeros(4, 64), 1)
 
 
+def test_binding_refuses_another_device(L, monkeypatch):
+    class Far:                        # a tensor of another GPU, as far as the check looks
+        shape = (4, 32)
+
+        def get_device(self):
+            return 3
+    with pytest.raises(ValueError, match="current device"):
+        rq.rq_mxfp4_dequantize(Far(), torch.zeros(512, dtype=torch.uint8), torch.zeros(4, 64), 1)
+
+
 # ------------------------------------------------------------------ GPU helpers
 def _rows(M, K, seed=0):
     rng = np.random.default_rng((seed, M, K))
