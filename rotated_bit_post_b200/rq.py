@@ -239,18 +239,33 @@ def rq_w4a4_linear2(M, N, K, a_codes, a_scale, a_zero_point, w_codes, w_scale, w
         _dev(Y), int(out_fp32), _dev(status), _stream(stream)))
 
 
-def _here(*tensors):
-    """The tensors lie on the current device, whose stream and kernels the call takes."""
-    import torch
-    here = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+def _devs(*tensors):
+    """Device pointers of contiguous tensors of the current device, whose
+    stream and kernels the call takes."""
+    out, here = [], None
     for t in tensors:
-        if t.get_device() not in (here, -1):   # (_dev refuses host tensors)
-            raise ValueError(f"tensor on device {t.get_device()}, the current device is {here}")
+        d = t.get_device()
+        if d != here:
+            if d < 0:
+                raise ValueError("device buffer expected (torch CUDA tensor)")
+            if here is None:
+                here = _current_device()
+            if d != here:
+                raise ValueError(f"tensor on device {d}, the current device is {here}")
+        if not t.is_contiguous():
+            raise ValueError("device buffers must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _current_device():
+    import torch
+    return torch._C._cuda_getDevice()   # (a CUDA tensor exists: nothing to initialise)
 
 
 def _shape(what, t, elem_bytes, n):
     """The buffer holds at least n elements of that many bytes."""
-    if t.element_size() != elem_bytes or t.numel() < n:
+    if t.numel() < n or t.element_size() != elem_bytes:
         raise ValueError(f"{what}: {n} elements of {elem_bytes} bytes expected, "
                          f"got {t.numel()} of {t.element_size()}")
 
@@ -258,11 +273,10 @@ def _shape(what, t, elem_bytes, n):
 def rq_mxfp4_dequantize(codes, block_scale, out, out_fp32, stream=None):
     """Values of MXFP4 codes [rows, K/2] -> out [rows, K], FP32 or BF16."""
     rows, K = codes.shape[0], codes.shape[1] * 2
-    _here(codes, block_scale, out)
     _shape("block_scale", block_scale, 1, mx_sf_bytes(rows, K))
     _shape("out", out, 4 if out_fp32 else 2, rows * K)
     _check("rq_mxfp4_dequantize", lib().rq_mxfp4_dequantize(
-        rows, K, _dev(codes), _dev(block_scale), _dev(out), int(out_fp32), _stream(stream)))
+        rows, K, *_devs(codes, block_scale, out), int(out_fp32), _stream(stream)))
 
 
 def rq_mxfp4_layer_workspace(M: int, N: int, K: int) -> int:
@@ -274,15 +288,15 @@ def rq_mxfp4_layer(X, block, rot, w_codes, w_bscale, workspace, Y, out_fp32, sta
     """Y = Q(R X) W^T from BF16 rows, MXFP4 on both sides."""
     M, K = X.shape
     N = w_codes.shape[0]
-    _here(X, rot, w_codes, w_bscale, workspace, Y, status)
     _shape("X", X, 2, M * K)
     _shape("rot", rot, 4, K)
     _shape("w_codes", w_codes, 1, N * (K // 2))
     _shape("w_bscale", w_bscale, 1, mx_sf_bytes(N, K))
     _shape("Y", Y, 4 if out_fp32 else 2, M * N)
+    x, r, w, s, ws, y, st = _devs(X, rot, w_codes, w_bscale, workspace, Y, status)
     _check("rq_mxfp4_layer", lib().rq_mxfp4_layer(
-        M, N, K, block, _dev(X), _dev(rot), _dev(w_codes), _dev(w_bscale), _dev(workspace),
-        workspace.numel() * workspace.element_size(), _dev(Y), int(out_fp32), _dev(status), _stream(stream)))
+        M, N, K, block, x, r, w, s, ws, workspace.numel() * workspace.element_size(), y, int(out_fp32), st,
+        _stream(stream)))
 
 
 def rq_mxfp4_moe_workspace(T: int, K: int, I: int, E: int, top_k: int) -> int:
@@ -296,7 +310,6 @@ def rq_mxfp4_moe(X, router, top_k, renorm, block, rot, w1_codes, w1_bscale, bloc
     rows), w2_codes [E, K, I/2]; routing out to topk_idx / topk_weight."""
     T, K = X.shape
     E, I = w1_codes.shape[0], w1_codes.shape[1] // 2
-    _here(X, router, rot, w1_codes, w1_bscale, w2_codes, w2_bscale, topk_idx, topk_weight, workspace, Y, status)
     _shape("X", X, 2, T * K)
     _shape("router", router, 2, E * K)
     _shape("rot", rot, 4, K)
@@ -307,10 +320,11 @@ def rq_mxfp4_moe(X, router, top_k, renorm, block, rot, w1_codes, w1_bscale, bloc
     _shape("topk_idx", topk_idx, 4, T * top_k)
     _shape("topk_weight", topk_weight, 4, T * top_k)
     _shape("Y", Y, 4 if out_fp32 else 2, T * K)
+    x, rt, r, w1, s1, w2, s2, ix, wt, ws, y, st = _devs(X, router, rot, w1_codes, w1_bscale, w2_codes, w2_bscale, topk_idx,
+                                                        topk_weight, workspace, Y, status)
     _check("rq_mxfp4_moe", lib().rq_mxfp4_moe(
-        T, K, I, E, top_k, int(renorm), _dev(X), _dev(router), block, _dev(rot), _dev(w1_codes), _dev(w1_bscale),
-        block2, _dev(w2_codes), _dev(w2_bscale), _dev(topk_idx), _dev(topk_weight), _dev(workspace),
-        workspace.numel() * workspace.element_size(), _dev(Y), int(out_fp32), _dev(status), _stream(stream)))
+        T, K, I, E, top_k, int(renorm), x, rt, block, r, w1, s1, block2, w2, s2, ix, wt, ws,
+        workspace.numel() * workspace.element_size(), y, int(out_fp32), st, _stream(stream)))
 
 
 def rq_read_status(status, stream=None):

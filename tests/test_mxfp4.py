@@ -154,14 +154,14 @@ def test_binding_checks_sizes(L):
         rq.rq_mxfp4_dequantize(c, s, torch.zeros(4, 64), 1)
 
 
-def test_binding_refuses_another_device(L, monkeypatch):
-    class Far:                        # a tensor of another GPU, as far as the check looks
-        shape = (4, 32)
+def test_binding_refuses_another_device(monkeypatch):
+    monkeypatch.setattr(rq, "_current_device", lambda: 0)
 
+    class Far:                        # a tensor of another GPU, as far as the check looks
         def get_device(self):
             return 3
-    with pytest.raises(ValueError, match="current device"):
-        rq.rq_mxfp4_dequantize(Far(), torch.zeros(512, dtype=torch.uint8), torch.zeros(4, 64), 1)
+    with pytest.raises(ValueError, match="tensor on device 3"):
+        rq._devs(Far())
 
 
 # ------------------------------------------------------------------ GPU helpers
