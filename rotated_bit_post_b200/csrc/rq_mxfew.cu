@@ -21,6 +21,10 @@
 //            hidden rows of tokens that did not choose an expert are zeros, so
 //            the sum over a token's experts happens in the accumulator
 //
+// Bound by the bytes of the weights where there are many (64 tokens, 128 experts of
+// 2048 x 768, top 8: gate/up 40 us at 5 TB/s, down 25 us), by latencies where there are
+// few (1 x 4096 x 12288, fused: 10.9 us of which the weights' bytes are 4.1).
+//
 // Per CTA: warp 0 issues the copies (weights and tokens by TMA, 256 columns =
 // 128 bytes a row per stage; scale tiles by bulk copies), warp 1 moves the
 // scales to TMEM and issues the MMAs, warps 4-7 drain the accumulator, all

@@ -10,6 +10,11 @@
 // 4-11 are the epilogue.  The accumulator takes 256 of the 512 TMEM columns and
 // is single: the epilogue brings it into registers as packed BF16 first, hands
 // it back, and stores while the next tile runs.
+//
+// 4608 x 12288 x 4096: 75 us, 6.2 PFLOP/s, tensor pipe 77% busy; a step of 256
+// columns takes 0.39 us, which is what its copies take without the MMAs (13 TB/s
+// from L2 over all SMs; the MMAs 0.27).  65520 x 1536 x 8960: 370-400 us, 0.8 of the
+// 3.2 us a tile between its last MMA and the next tile's first.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -331,6 +331,49 @@ def test_dequantize(L, rows, K):
         out = torch.empty((rows, K), dtype=dt, device="cuda")
         rq.rq_mxfp4_dequantize(codes, sf, out, fp32)
         assert np.array_equal(out.double().cpu().numpy(), ref, equal_nan=True)   # every value is exact in BF16
+        # an output that is 16-byte aligned and no more, with its neighbours untouched
+        n, off = rows * K, 16 // out.element_size()
+        wide = torch.full((n + 2 * off,), 7.0, dtype=dt, device="cuda")
+        rq.rq_mxfp4_dequantize(codes, sf, wide[off: off + n], fp32)
+        assert np.array_equal(wide[off: off + n].view(rows, K).double().cpu().numpy(), ref, equal_nan=True)
+        assert (wide[:off] == 7).all() and (wide[off + n:] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,block", [(2, 200, 512, 128), (30, 136, 512, 128), (150, 264, 512, 128)])
+def test_layer_on_16_byte_aligned_buffers(L, M, N, K, block):
+    # every buffer 16 bytes into its allocation: the alignment that the calls ask for, and no more
+    X, rot_t, wc, wsf, A, B = _layer_case(M, N, K, block)
+
+    def shifted(t):
+        off = 16 // t.element_size()
+        s = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")[off:]
+        return s.copy_(t.reshape(-1)).view(t.shape)
+    ws, st = shifted(_workspace(rq.rq_mxfp4_layer_workspace(M, N, K))), _status()
+    for dt in (torch.float32, torch.bfloat16):
+        Y = shifted(torch.zeros((M, N), dtype=dt, device="cuda"))
+        rq.rq_mxfp4_layer(shifted(X), block, shifted(rot_t), shifted(wc), shifted(wsf), ws, Y, int(dt == torch.float32), st)
+        _ok(st)
+        # FP32 sums, then half a step of the output's type
+        ref = A @ B.T
+        assert (np.abs(Y.double().cpu().numpy() - ref) <= _sum_bound(A, B) * 1.01 +
+                (np.abs(ref) + _sum_bound(A, B)) * torch.finfo(dt).eps / 2).all()
+
+
+@pytest.mark.gpu
+def test_moe_on_16_byte_aligned_buffers(L):
+    m = Moe(5, 192, 128, 4, 2, True, 64, 32)
+    idx, w, Y = m.run()
+
+    def shifted(t):
+        off = 16 // t.element_size()
+        s = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")[off:]
+        return s.copy_(t.reshape(-1)).view(t.shape)
+    m.w1, m.w2 = tuple(map(shifted, m.w1)), tuple(map(shifted, m.w2))
+    m.router_t, m.rot_t = shifted(_cuda(m.router)), shifted(torch.from_numpy(m.rot).cuda())
+    bufs = tuple(map(shifted, m.out()))
+    got = m.run(bits=shifted(_cuda(m.bits)), bufs=bufs)
+    assert all(torch.equal(a, b) for a, b in zip(got, (idx, w, Y)))
 
 
 # ------------------------------------------------------------------ GPU: product
