@@ -138,6 +138,7 @@ __device__ __forceinline__ uint32_t few_idesc(int n, uint32_t id) {
 enum { LINEAR = 0, GATE_UP = 1, DOWN = 2, FUSED = 3 };
 constexpr int FUSED_SF = 512;           // FUSED: scale bytes per step, two tiles 256 bytes apart: the rows past
                                         // the 16th that a tile's copy also brings are other tiles', not used
+constexpr int FUSED_MIN_STAGES = 3;     // see launch_mode
 constexpr int FUSED_THREADS = 384;
 constexpr int FUSED_WARPS = FUSED_THREADS / 32 - 2;   // all but the first two transform the rows
 __host__ __device__ constexpr int few_threads(int mode) { return mode == FUSED ? FUSED_THREADS : FEW_THREADS; }
@@ -516,20 +517,29 @@ cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int s
   int S = 1;
   while (S < 8 && (int64_t)tiles * ny * 2 * S <= fill && 4 * S <= steps) S *= 2;
   const int stage = NA * (128 * 128 + 1024) + (MODE == FUSED ? 0 : p.NT * 128 + 1024);
-  const int most = (steps + S - 1) / S;
-  // FUSED: the token codes and scales of every step, the rows, the table's entries
-  const int U = p.block < 64 ? 64 : p.block;
-  const int x_bytes = MODE == FUSED ? (most * (p.NT * 128 + FUSED_SF) + 256 + 1023) & ~1023 : 0;
-  const int rows_bytes = MODE == FUSED ? (p.T * p.K * 2 + 1023) & ~1023 : 0;
-  const int rot_bytes = MODE == FUSED ? ((most * 256 + 2 * U) * 4 + 1023) & ~1023 : 0;
-  const int fixed = x_bytes + rows_bytes + rot_bytes;
   const int parts = (NA * p.NT * FEW_PITCH * 4 + 1023) & ~1023;   // the partial sums overlay the stages
-  // one CTA per SM, shared memory full of stages, if all are resident that way (a
-  // cluster's CTAs lie in one group of SMs: 148, 148, 132 and 120 for clusters of
-  // 1, 2, 4 and 8 on 148 SMs); otherwise two share an SM
-  const int64_t room = S <= 2 ? sms : S == 4 ? sms * 8 / 9 : sms * 4 / 5;
-  const int limit = (int64_t)tiles * ny * S > room ? 115712 : 230400;
-  p.stages = (limit - FEW_TAIL - 1024 - fixed) / stage;
+  int x_bytes = 0, rows_bytes = 0;   // FUSED: the token codes and scales of every step, the rows, the table's entries
+  int rot_bytes = 0, most;
+  for (;; S /= 2) {
+    most = (steps + S - 1) / S;
+    if constexpr (MODE == FUSED) {
+      const int U = p.block < 64 ? 64 : p.block;
+      x_bytes = (most * (p.NT * 128 + FUSED_SF) + 256 + 1023) & ~1023;
+      rows_bytes = (p.T * p.K * 2 + 1023) & ~1023;
+      rot_bytes = ((most * 256 + 2 * U) * 4 + 1023) & ~1023;
+    }
+    // one CTA per SM, shared memory full of stages, if all are resident that way (a
+    // cluster's CTAs lie in one group of SMs: 148, 148, 132 and 120 for clusters of
+    // 1, 2, 4 and 8 on 148 SMs); otherwise two share an SM
+    const int64_t room = S <= 2 ? sms : S == 4 ? sms * 8 / 9 : sms * 4 / 5;
+    const int limit = (int64_t)tiles * ny * S > room ? 115712 : 230400;
+    p.stages = (limit - FEW_TAIL - 1024 - x_bytes - rows_bytes - rot_bytes) / stage;
+    // FUSED: beside long rows half an SM has room for few stages or none; fewer
+    // ranks with a whole SM each then (us for 1 x 6144 x 14336, blocks of 1024: 28.8 with
+    // two stages, 26.6 this way; 2 x 8192 x 18944, blocks of 512: 45.1 with one, 38.9;
+    // with three stages half an SM is as good or better: 4 x 4096 x 12288 24.6, 26.6)
+    if (MODE != FUSED || S == 1 || p.stages >= FUSED_MIN_STAGES) break;
+  }
   if (p.stages < 1) return cudaErrorInvalidValue;
   if (p.stages > FEW_MAX_STAGES) p.stages = FEW_MAX_STAGES;
   if (p.stages > most) p.stages = most < 1 ? 1 : most;

@@ -466,7 +466,8 @@ def _workspace(n):
                                          (64, 256, 8192, 256), (65, 256, 256, 64), (200, 640, 1152, 128),
                                          (2, 64, 16384, 512), (4, 300, 4096, 1024), (2, 640, 8192, 512),
                                          (1, 2305, 1024, 32), (3, 2048, 1344, 64), (1, 129, 8192, 1024),
-                                         (4, 4300, 256, 16), (1, 18900, 512, 256), (2, 4200, 1088, 64)])
+                                         (4, 4300, 256, 16), (1, 18900, 512, 256), (2, 4200, 1088, 64),
+                                         (2, 9473, 8192, 1024), (1, 9600, 6144, 1024)])
 def test_layer(L, M, N, K, block):
     X, rot_t, wc, wsf, A, B = _layer_case(M, N, K, block)
     ws, st = _workspace(rq.rq_mxfp4_layer_workspace(M, N, K)), _status()
