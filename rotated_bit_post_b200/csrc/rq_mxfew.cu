@@ -284,13 +284,15 @@ __global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __gr
       const uint64_t d_op = smem_desc(sbase, 16, 1024, 2), d_sf = smem_desc(sbase + NA * PA + (MODE == FUSED ? 0 : PB), 16, 128, 0);
       const uint64_t d_x = smem_desc(sbase + (MODE == FUSED ? p.off_x : NA * PA), 16, 1024, 2);
       const uint64_t d_xsf = smem_desc(sbase + (MODE == FUSED ? p.off_x + n * PB : NA * PA + PB + NA * SF), 16, 128, 0);
-      // No wait here hands out an answer: with a branch on one the compiler no
-      // longer takes what follows for warp-uniform.  After a wait has run out the
-      // others return at once and the loop runs to its end on whatever is there.
-      if (MODE == FUSED) mbar_wait_soon(xready, 0, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+      // No branch is taken on a wait's answer: with one the compiler no longer takes
+      // what follows for warp-uniform.  After a wait has run out the loop runs to its
+      // end on whatever is there, but frees no stage any more: a copy into a stage whose
+      // last copies are still out would arrive on a barrier that expects no arrival.
+      bool ok = true;
+      if (MODE == FUSED) ok = mbar_wait_soon(xready, 0, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
       const uint32_t id0 = few_idesc(p.NT, 0), id2 = few_idesc(p.NT, 2);
       for (int i = 0; i < n; ++i) {
-        mbar_wait_soon(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+        ok &= mbar_wait_soon(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
         tc_fence_after();
         const int sct = min(2, KT - kt * 2), kkn = min(4, p.K / 64 - kt * 4);
         const uint32_t st = (uint32_t)(s * STAGE) >> 4;
@@ -314,8 +316,8 @@ __global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __gr
                 umma_mxf4(tmem + h * p.NT, d_op + st + ((h * PA + kk * 32) >> 4), d_x + xst + ((kk * 32) >> 4),
                           kk & 1 ? id2 : id0, tsf + h * 8 + (kk >> 1) * 4, tsf + NA * 8 + (kk >> 1) * 4, i > 0 || kk > 0);
             }
-          tc_commit(&empty[s]);
-          if (i == n - 1) tc_commit(accfull);
+          tc_commit_if(&empty[s], ok);
+          if (i == n - 1) tc_commit_if(accfull, ok);
         }
         if (++s == p.stages) { s = 0; ph ^= 1; }
         if (++kt == spe) kt = 0;

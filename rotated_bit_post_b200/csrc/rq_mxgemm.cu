@@ -257,13 +257,15 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
       int s = 0, ph = 0, acc_ph = 1;
       // descriptors of the first stage; the address field counts 16-byte units
       const uint64_t d_op = smem_desc(sbase, 16, 1024, 2), d_sf = smem_desc(sbase + MG_PA + MG_PB, 16, 128, 0);
-      // No wait here hands out an answer: with a branch on one the compiler no
-      // longer takes what follows for warp-uniform.  After a wait has run out the
-      // others return at once, and the loop ends with its tile.
+      // No branch is taken on a wait's answer: with one the compiler no longer takes
+      // what follows for warp-uniform.  After a wait has run out the loop ends with its
+      // tile, but frees no stage any more: a copy into a stage whose last copies are
+      // still out would arrive on a barrier that expects no arrival.
+      bool ok = true;
       for (int tile = tile0; tile < ntiles; tile += tstep) {
         if (uniform(*abort_flag)) break;
         for (int kt = 0; kt < nk; ++kt) {
-          mbar_wait_soon(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
+          ok &= mbar_wait_soon(&full[s], ph, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
           tc_fence_after();
           const uint32_t st = (uint32_t)(s * MG_STAGE) >> 4;
           // the scales to the stage's own TMEM columns, free again when the stage is
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
             }
           }
           if (kt == 0) {   // (the first tile finds the accumulator empty)
-            mbar_wait_soon(accempty, acc_ph, p.status, ST_TIMEOUT_EPI, abort_flag, p.wait_ns);
+            ok &= mbar_wait_soon(accempty, acc_ph, p.status, ST_TIMEOUT_EPI, abort_flag, p.wait_ns);
             acc_ph ^= 1;
             tc_fence_after();
           }
@@ -289,8 +291,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
               if (kk < kkn)
                 umma_mxf4_2(tmem, d_op + st + ((kk * 32) >> 4), d_op + st + ((MG_PA + kk * 32) >> 4), mg_idesc((kk & 1) * 2),
                             tsf + (kk >> 1) * 4, tsf + 8 + (kk >> 1) * 8, kt > 0 || kk > 0);
-            tc_commit2_mc(&empty[s], 0x3);
-            if (kt == nk - 1) tc_commit2_mc(accfull, 0x3);
+            tc_commit2_mc_if(&empty[s], 0x3, ok);
+            if (kt == nk - 1) tc_commit2_mc_if(accfull, 0x3, ok);
           }
           if (++s == MG_STAGES) { s = 0; ph ^= 1; }
         }

@@ -247,6 +247,14 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+// The same where `go` holds, without a branch that the compiler sees.
+__device__ __forceinline__ void tc_commit_if(uint64_t* bar, bool go) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"((int)go)
+      : "memory");
+}
 
 // Completion of this thread's earlier pair MMAs arrives once on the barrier at
 // the same offset in every CTA of `mask` (a tcgen05 commit, not a data copy).
@@ -255,6 +263,15 @@ __device__ __forceinline__ void tc_commit2_mc(uint64_t* bar, uint16_t mask) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
       "h"(mask)
+      : "memory");
+}
+// The same where `go` holds, without a branch that the compiler sees.
+__device__ __forceinline__ void tc_commit2_mc_if(uint64_t* bar, uint16_t mask, bool go) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"(mask), "r"((int)go)
       : "memory");
 }
 // CTA-pair FP8 MMA, issued by the even CTA: M = 256 rows (128 from each CTA's
