@@ -37,10 +37,14 @@ rq_status rq_convert_check(const float* in, int32_t n, uint8_t* e4m3, uint8_t* e
  * bounded; this sets the bound, in nanoseconds, for launches made after the
  * call (from any thread).  0 restores the default of 2 s; values above 20 s
  * return RQ_ERR_INVALID_ARG.  `previous` (may be NULL) receives the old bound.
+ * The clock is read between attempts that suspend the thread for up to 1 ms
+ * each, at the latest after the third: a wait that runs out takes up to 4 ms
+ * longer than the bound.
  * A kernel whose wait runs out records a code in the caller's status word
  * (rq_read_status then returns RQ_ERR_TIMEOUT), stops issuing copies and
- * MMAs, waits (bounded) for the ones already issued, frees its tensor memory
- * and exits; the outputs of that call are undefined.
+ * MMAs (an MXFP4 product's MMAs within eight steps of 256 columns), waits
+ * (bounded) for the ones already issued, frees its tensor memory and exits;
+ * the outputs of that call are undefined.
  */
 rq_status rq_set_wait_limit(uint64_t limit_ns, uint64_t* previous);
 

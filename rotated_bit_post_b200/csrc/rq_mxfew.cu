@@ -285,9 +285,9 @@ __global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __gr
       const uint64_t d_x = smem_desc(sbase + (MODE == FUSED ? p.off_x : NA * PA), 16, 1024, 2);
       const uint64_t d_xsf = smem_desc(sbase + (MODE == FUSED ? p.off_x + n * PB : NA * PA + PB + NA * SF), 16, 128, 0);
       // No branch is taken on a wait's answer: with one the compiler no longer takes
-      // what follows for warp-uniform.  After a wait has run out the loop runs to its
-      // end on whatever is there, but frees no stage any more: a copy into a stage whose
-      // last copies are still out would arrive on a barrier that expects no arrival.
+      // what follows for warp-uniform.  After a wait has run out the loop ends within
+      // eight steps on whatever is there, but frees no stage any more: a copy into a stage
+      // whose last copies are still out would arrive on a barrier that expects no arrival.
       bool ok = true;
       if (MODE == FUSED) ok = mbar_wait_soon(xready, 0, p.status, ST_TIMEOUT_FULL, abort_flag, p.wait_ns);
       const uint32_t id0 = few_idesc(p.NT, 0), id2 = few_idesc(p.NT, 2);
@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __gr
         }
         if (++s == p.stages) { s = 0; ph ^= 1; }
         if (++kt == spe) kt = 0;
+        if ((i & 7) == 7 && uniform(*abort_flag)) break;
       }
       if (*abort_flag) {   // wait (bounded) for the MMAs issued
         if (one) tc_commit(mdrain);

@@ -258,9 +258,9 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
       // descriptors of the first stage; the address field counts 16-byte units
       const uint64_t d_op = smem_desc(sbase, 16, 1024, 2), d_sf = smem_desc(sbase + MG_PA + MG_PB, 16, 128, 0);
       // No branch is taken on a wait's answer: with one the compiler no longer takes
-      // what follows for warp-uniform.  After a wait has run out the loop ends with its
-      // tile, but frees no stage any more: a copy into a stage whose last copies are
-      // still out would arrive on a barrier that expects no arrival.
+      // what follows for warp-uniform.  After a wait has run out the loop ends within
+      // eight steps, but frees no stage any more: a copy into a stage whose last copies
+      // are still out would arrive on a barrier that expects no arrival.
       bool ok = true;
       for (int tile = tile0; tile < ntiles; tile += tstep) {
         if (uniform(*abort_flag)) break;
@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(const __grid_con
             if (kt == nk - 1) tc_commit2_mc_if(accfull, 0x3, ok);
           }
           if (++s == MG_STAGES) { s = 0; ph ^= 1; }
+          if ((kt & 7) == 7 && uniform(*abort_flag)) break;
         }
       }
       if (*abort_flag) {   // wait (bounded) for the MMAs issued

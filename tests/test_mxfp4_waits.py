@@ -103,3 +103,33 @@ def test_expert_layer_of_many_steps(L, T, K, I, E, k):
     ws = torch.empty(rq.rq_mxfp4_moe_workspace(T, K, I, E, k), dtype=torch.uint8, device="cuda")
     _runs_out_then_recovers(lambda: rq.rq_mxfp4_moe(
         X, R, k, True, 64, rot_t, w1, s1, 64, w2, s2, idx, wt, ws, Y, 1, st), [Y, idx, wt], st)
+
+
+# A wait that runs out takes its limit of 5 ms and up to 4 ms of attempts; the bounded wait for the copies
+# already issued as long again; the steps still issued, and the launch, are microseconds.  2 x 9 ms, and
+# as much again for a machine that is shared.
+ENDS_WITHIN_MS = 36.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 64, 65, 300])
+def test_long_product_ends_soon_after_a_wait_runs_out(L, M):
+    # 4096 steps of 256 columns, 512 for each of eight ranks in the few-token form: what is left of them
+    # when the first wait runs out must not take an attempt each
+    N, K = 64, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a, sa, w, sw = _codes(g, M, K // 2), _scale(g, rq.mx_sf_bytes(M, K)), _codes(g, N, K // 2), _scale(g, rq.mx_sf_bytes(N, K))
+    Y, st = torch.empty((M, N), device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    took = []
+
+    def call():
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        rq.rq_w4a4_linear(rq.MXFP4, rq.MXFP4, M, N, K, a, None, sa, w, None, sw, None, None, None, None, Y, 1, st)
+        e1.record()
+        e1.synchronize()
+        took.append(e0.elapsed_time(e1))
+    _runs_out_then_recovers(call, [Y], st)
+    # normal, expired, normal, expired, normal
+    assert all(5.0 <= ms <= ENDS_WITHIN_MS for ms in took[1::2]), took
+    assert all(ms < 5.0 for ms in took[2::2]), took
