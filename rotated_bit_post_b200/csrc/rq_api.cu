@@ -432,18 +432,20 @@ rq_status rq_mxfp4_dequantize(int32_t rows, int32_t K, const uint8_t* codes, con
   return ok();
 }
 
+static bool layer_shape(int32_t M, int32_t N, int32_t K) { return M >= 0 && N > 0 && K > 0 && K % 64 == 0; }
+
 int64_t rq_mxfp4_layer_workspace(int32_t M, int32_t N, int32_t K) {
-  if (M < 0 || N <= 0 || K <= 0 || K % 64) return -1;
+  if (!layer_shape(M, N, K) || K > 16384) return -1;
   return up256((int64_t)M * (K / 2)) + up256(mx_tiles(M, K));
 }
 
 rq_status rq_mxfp4_layer(int32_t M, int32_t N, int32_t K, int32_t block, const uint16_t* X, const int32_t* rot,
                          const uint8_t* w_codes, const uint8_t* w_bscale, void* workspace, int64_t workspace_bytes,
                          void* Y, int32_t out_fp32, int32_t* status, void* stream) {
-  const int64_t need = rq_mxfp4_layer_workspace(M, N, K);
-  if (need < 0) return fail(RQ_ERR_INVALID_ARG, "bad shape M=%d N=%d K=%d (K %% 64 == 0)", M, N, K);
+  if (!layer_shape(M, N, K)) return fail(RQ_ERR_INVALID_ARG, "bad shape M=%d N=%d K=%d (K %% 64 == 0)", M, N, K);
   rq_status s = check_block(K, block);
   if (s != RQ_OK) return s;
+  const int64_t need = rq_mxfp4_layer_workspace(M, N, K);
   if (workspace_bytes < need)
     return fail(RQ_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
   if (M == 0) return ok();   // an empty tensor's pointer may be null
