@@ -263,8 +263,12 @@ def _current_device():
     return torch._C._cuda_getDevice()   # (a CUDA tensor exists: nothing to initialise)
 
 
-def _shape(what, t, elem_bytes, n):
-    """The buffer holds at least n elements of that many bytes."""
+def _shape(what, t, elem_bytes, n, width=0):
+    """The buffer holds at least n elements of that many bytes.  With a width,
+    one of more dimensions has rows of so many elements, n elements in all: rows
+    of another pitch would be read as other values."""
+    if width and t.dim() > 1 and (t.size(-1) != width or t.numel() != n):
+        raise ValueError(f"{what}: {n} elements in rows of {width} expected, got shape {tuple(t.shape)}")
     if t.numel() < n or t.element_size() != elem_bytes:
         raise ValueError(f"{what}: {n} elements of {elem_bytes} bytes expected, "
                          f"got {t.numel()} of {t.element_size()}")
@@ -290,7 +294,7 @@ def rq_mxfp4_layer(X, block, rot, w_codes, w_bscale, workspace, Y, out_fp32, sta
     N = w_codes.shape[0]
     _shape("X", X, 2, M * K)
     _shape("rot", rot, 4, K)
-    _shape("w_codes", w_codes, 1, N * (K // 2))
+    _shape("w_codes", w_codes, 1, N * (K // 2), K // 2)
     _shape("w_bscale", w_bscale, 1, mx_sf_bytes(N, K))
     _shape("Y", Y, 4 if out_fp32 else 2, M * N)
     x, r, w, s, ws, y, st = _devs(X, rot, w_codes, w_bscale, workspace, Y, status)
@@ -307,15 +311,18 @@ def rq_mxfp4_moe_workspace(T: int, K: int, I: int, E: int, top_k: int) -> int:
 def rq_mxfp4_moe(X, router, top_k, renorm, block, rot, w1_codes, w1_bscale, block2, w2_codes, w2_bscale, topk_idx,
                  topk_weight, workspace, Y, out_fp32, status, stream=None):
     """Mixture-of-experts layer: w1_codes [E, 2I, K/2] (gate rows, then up
-    rows), w2_codes [E, K, I/2]; routing out to topk_idx / topk_weight."""
+    rows), w2_codes [E, K, I/2] (or flat, as router [E, K]); routing out to
+    topk_idx / topk_weight."""
     T, K = X.shape
-    E, I = w1_codes.shape[0], w1_codes.shape[1] // 2
+    if w1_codes.dim() != 3 or w1_codes.size(1) % 2:
+        raise ValueError(f"w1_codes: [E, 2I, K/2] expected, got shape {tuple(w1_codes.shape)}")
+    E, I = w1_codes.size(0), w1_codes.size(1) // 2
     _shape("X", X, 2, T * K)
-    _shape("router", router, 2, E * K)
+    _shape("router", router, 2, E * K, K)
     _shape("rot", rot, 4, K)
-    _shape("w1_codes", w1_codes, 1, E * 2 * I * (K // 2))
+    _shape("w1_codes", w1_codes, 1, E * 2 * I * (K // 2), K // 2)
     _shape("w1_bscale", w1_bscale, 1, E * mx_sf_bytes(2 * I, K))
-    _shape("w2_codes", w2_codes, 1, E * K * (I // 2))
+    _shape("w2_codes", w2_codes, 1, E * K * (I // 2), I // 2)
     _shape("w2_bscale", w2_bscale, 1, E * mx_sf_bytes(K, I))
     _shape("topk_idx", topk_idx, 4, T * top_k)
     _shape("topk_weight", topk_weight, 4, T * top_k)
