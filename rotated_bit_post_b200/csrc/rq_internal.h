@@ -142,8 +142,10 @@ bool mx_scale_map(CUtensorMap* m, const uint8_t* sf, uint64_t rows, uint64_t col
 bool mx_out_map(CUtensorMap* m, void* Y, uint64_t rows, uint64_t cols);
 // MXFP4 products of more tokens, without the low-rank branch (rq_mxgemm.cu)
 cudaError_t launch_mx_gemm(const GemmLaunch& a, cudaStream_t st, const char** why);
-// MXFP4 products of at most MX_FEW_TOKENS tokens (rq_mxfew.cu)
+// MXFP4 products of at most MX_FEW_TOKENS tokens (rq_mxfew.cu); with the low-rank
+// branch only where mx_few_low_rank says so
 constexpr int MX_FEW_TOKENS = 64;
+bool mx_few_low_rank(int M, int N, int K, int r, int sms);
 cudaError_t launch_mx_few(const GemmLaunch& a, cudaStream_t st, const char** why);
 // the whole layer from BF16 rows in one launch, for the shapes it takes
 bool mx_layer_fused(int M, int N, int K, int sms);

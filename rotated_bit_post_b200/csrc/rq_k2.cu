@@ -1529,7 +1529,8 @@ cudaError_t launch_pair(Kern k, int smem, int pairs, int threads, const TMaps& t
 }  // namespace
 
 cudaError_t launch_gemm(const GemmLaunch& a, cudaStream_t st, const char** why) {
-  if (a.a_fmt == RQ_FMT_MXFP4 && a.M <= MX_FEW_TOKENS) return launch_mx_few(a, st, why);
+  if (a.a_fmt == RQ_FMT_MXFP4 && a.M <= MX_FEW_TOKENS && (!a.c || mx_few_low_rank(a.M, a.N, a.K, a.r, a.num_sms)))
+    return launch_mx_few(a, st, why);
   if (a.a_fmt == RQ_FMT_MXFP4 && !a.c) return launch_mx_gemm(a, st, why);
   TMaps tm;
   memset(&tm, 0, sizeof(tm));

@@ -504,6 +504,14 @@ __global__ void __launch_bounds__(few_threads(MODE), 2) mx_few_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ host side
+// Ranks per cluster: as many as keep the grid within `fill` CTAs, two steps each at
+// least.  33 tiles of 32 steps: 12.7, 9.9, 8.4, 9.1 us with 1, 2, 4, 8 ranks.
+int few_ranks(int64_t clusters, int steps, int fill) {
+  int S = 1;
+  while (S < 8 && clusters * 2 * S <= fill && 4 * S <= steps) S *= 2;
+  return S;
+}
+
 // `tiles` x `ny` clusters, `steps` K steps to split.
 template <int MODE>
 cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int steps, int sms, cudaStream_t st) {
@@ -511,14 +519,11 @@ cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int s
   static SmemLimit limit_once;
   cudaError_t e = limit_once.raise(reinterpret_cast<const void*>(mx_few_kernel<MODE>));
   if (e != cudaSuccess) return e;
-  // Ranks per cluster: as many as leave every CTA an SM, two steps each at
-  // least.  33 tiles of 32 steps: 12.7, 9.9, 8.4, 9.1 us with 1, 2, 4, 8 ranks.  The
-  // gate/up products split only while half the SMs are left, where the down
-  // products' CTAs start and fetch their weights early (64 tiles: 19.6 us for
-  // the layer with 1 rank, 21.2 with 2).
+  // An SM for every CTA (FUSED: half an SM).  The gate/up products split only while
+  // half the SMs are left, where the down products' CTAs start and fetch their
+  // weights early (64 tiles: 19.6 us for the layer with 1 rank, 21.2 with 2).
   const int fill = MODE == GATE_UP ? sms / 2 : MODE == FUSED ? 2 * sms : sms;
-  int S = 1;
-  while (S < 8 && (int64_t)tiles * ny * 2 * S <= fill && 4 * S <= steps) S *= 2;
+  int S = few_ranks((int64_t)tiles * ny, steps, fill);
   const int stage = NA * (128 * 128 + 1024) + (MODE == FUSED ? 0 : p.NT * 128 + 1024);
   const int parts = (NA * p.NT * FEW_PITCH * 4 + 1023) & ~1023;   // the partial sums overlay the stages
   int x_bytes = 0, rows_bytes = 0;   // FUSED: the token codes and scales of every step, the rows, the table's entries
@@ -581,6 +586,18 @@ cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int s
 int token_columns(int T) { return (T + 15) / 16 * 16; }
 
 }  // namespace
+
+// With the low-rank branch the epilogue reads r values of L for each of a rank's
+// tokens, one after another: about r (4 + tokens per rank), as against the longer
+// way of the one-CTA kernel of rq_k2.cu (128 x 128 tiles, no split of K) through K,
+// about K / 32 in the same unit.  us here and there: 64 x 4096 x 12288, r = 32: 153.6
+// and 12.4; r = 8: 29.0 and 12.5, for 8 tokens 11.9 and 12.7; 4096 outputs of 16384
+// columns, r = 32, 32 and 64 tokens: 29.9 and 31.0, 48.7 and 31.1; of 8192 columns, 8 and
+// 16 tokens: 15.8 and 17.8, 19.5 and 17.8; 1 x 1152 x 1152, r = 8: 5.7 and 5.5.
+bool mx_few_low_rank(int M, int N, int K, int r, int sms) {
+  const int S = few_ranks((N + 127) / 128, (K + 255) / 256, sms > 0 ? sms : 148);
+  return r * (4 + (M + S - 1) / S) * 32 < K;
+}
 
 cudaError_t launch_mx_few(const GemmLaunch& a, cudaStream_t st, const char** why) {
   FewMaps tm;

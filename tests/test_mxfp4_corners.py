@@ -45,7 +45,8 @@ def test_wide_expert_layers(L, T, K, I, E, k):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,N,K,r", [(1, 132, 192, 32), (64, 300, 320, 24), (65, 129, 256, 8), (200, 300, 1152, 32)])
+@pytest.mark.parametrize("M,N,K,r", [(1, 132, 192, 32), (64, 300, 320, 24), (65, 129, 256, 8), (200, 300, 1152, 32),
+                                     (1, 132, 8192, 32), (4, 101, 4096, 8), (8, 520, 8192, 16), (64, 260, 16384, 16)])
 def test_low_rank_product_in_bf16(L, M, N, K, r):
     rng = np.random.default_rng((M, r))
     ac, asf, A = mx._packed(rng.standard_normal((M, K)).astype(np.float32))
@@ -60,3 +61,36 @@ def test_low_rank_product_in_bf16(L, M, N, K, r):
     ref, near = A @ B.T, mx._sum_bound(A, B)
     y = Y[: M * N].view(M, N).double().cpu().numpy()
     assert (np.abs(y - ref) <= near + (np.abs(ref) + near) * 2.0 ** -8).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,r", [(64, 12288, 4096, 32), (64, 4608, 1152, 32), (16, 1152, 1152, 16)])
+def test_low_rank_branch_has_no_cliff(L, M, N, K, r):
+    # up to 64 tokens a product may take the few-token kernel, whose low-rank branch costs r per token in
+    # the epilogue; one token more never does.  The same work within a factor of three (it was 12 to 14).
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w, sw = (torch.randint(0, 256, (n,), dtype=torch.uint8, device="cuda", generator=g) for n in (N * K // 2, rq.mx_sf_bytes(N, K)))
+    Lr, st = torch.zeros((N, r), dtype=torch.int16, device="cuda"), mx._status()
+
+    def us(m):
+        a, sa = torch.zeros((m, K // 2), dtype=torch.uint8, device="cuda"), torch.zeros(rq.mx_sf_bytes(m, K), dtype=torch.uint8, device="cuda")
+        c, Y = torch.zeros((m, r), dtype=torch.int16, device="cuda"), torch.empty((m, N), dtype=torch.bfloat16, device="cuda")
+        call = lambda: rq.rq_w4a4_linear(rq.MXFP4, rq.MXFP4, m, N, K, a, None, sa, w.view(N, K // 2), None, sw, None, None, c, Lr, Y, 0, st)  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(10):
+                call()
+        took = []
+        for _ in range(9):
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record()
+            graph.replay()
+            e1.record()
+            e1.synchronize()
+            took.append(e0.elapsed_time(e1) * 100)
+        return sorted(took)[4]
+    few, more = us(M), us(65)
+    mx._ok(st)
+    assert few < 3 * more, (few, more)
