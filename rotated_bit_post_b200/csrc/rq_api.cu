@@ -92,7 +92,8 @@ rq_status check_rows_call(int32_t fmt, bool weight, const void* X, int32_t rows,
     if (!coef) return fail(RQ_ERR_INVALID_ARG, "U given without a coefficient output");
     if (!aligned16(U) || !aligned16(coef)) return fail(RQ_ERR_ALIGNMENT, "U / coefficient output not 16-byte aligned");
   }
-  if (!aligned16(X) || !aligned16(rot) || !aligned16(codes) || !aligned16(scale) || (bscale && !aligned16(bscale)))
+  if (!aligned16(X) || !aligned16(rot) || !aligned16(codes) || (!aligned16(scale) && fmt != RQ_MXFP4) ||
+      (bscale && !aligned16(bscale)))
     return fail(RQ_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
   return RQ_OK;
 }
@@ -362,7 +363,7 @@ static rq_status linear_impl(int32_t a_fmt, int32_t w_fmt, int32_t M, int32_t N,
     return fail(RQ_ERR_UNSUPPORTED, "low-rank branch supports r in {8, 16, 24, 32} (got %d)", r);
   if (c && (a_fmt == RQ_INT8 || a_fmt == RQ_INT4A))
     return fail(RQ_ERR_UNSUPPORTED, "the low-rank branch runs with 4-bit activations");
-  const void* ptrs[] = {a_codes, a_scale, w_codes, w_scale, Y, a_bscale, w_bscale, c, L};
+  const void* ptrs[] = {a_codes, mx ? nullptr : a_scale, w_codes, mx ? nullptr : w_scale, Y, a_bscale, w_bscale, c, L};
   for (const void* q : ptrs)
     if (q && !aligned16(q)) return fail(RQ_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
   if (M == 0) return ok();

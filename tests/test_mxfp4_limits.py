@@ -82,3 +82,16 @@ def test_expert_layer_takes_flat_weights(L):
     for kw in ({}, {"w2": _u8(4 * 128 * 64)}, {"w2": _u8(4 * 128, 64)}, {"router": torch.zeros(4 * 128, dtype=torch.bfloat16)}):
         with pytest.raises(ValueError, match="device buffer"):
             _moe(**kw)
+
+
+def test_row_scales_are_ignored(L):
+    # MXFP4 has none: whatever stands in their place is not looked at
+    odd = ctypes.c_void_p(0x1004)
+    for scale in (None, P, odd):
+        assert L.rq_rotate_quantize_act(rq.MXFP4, P, 0, 128, 64, P, None, None, 0, None, P, scale, P, None, None) == 0
+        assert L.rq_quantize_weights(rq.MXFP4, P, 0, 128, 64, P, None, None, 0, None, P, scale, P, None, None) == 0
+        assert L.rq_w4a4_linear(rq.MXFP4, rq.MXFP4, 0, 5, 128, P, scale, P, P, scale, P, None, None, None, None, 0, P, 0,
+                                None, None) == 0
+    assert L.rq_rotate_quantize_act(rq.NVFP4, P, 0, 128, 64, P, None, None, 0, None, P, odd, P, None, None) == 3
+    assert L.rq_w4a4_linear(rq.NVFP4, rq.NVFP4, 0, 5, 128, P, odd, P, P, P, P, None, None, None, None, 0, P, 0,
+                            None, None) == 3
