@@ -13,7 +13,8 @@ W2A4 MLP with CFG (65520 tokens x 1536 -> 8960); with ``--config all`` (the
 default) the other four layers, and the PixArt-like fc1 layer with the full PCA
 rotation in place of RPBH (``c2p``: K1 is then rq_pca_rotate_quantize_act, a
 BF16 tensor-core product x V plus the split/quantize pass), are timed in the
-same run and reported under ``configs``.  Multi-GPU (torchrun): every rank runs the same layers on its own
+same run and reported under ``configs``, one row of figures each (``us``: the
+step, K1, K2; ``--details FILE`` writes everything).  Multi-GPU (torchrun): every rank runs the same layers on its own
 token batches (weak scaling, no collective on the data path); times are the
 max over ranks.  ``--impl reference`` times the CPU oracle on the host cores on
 a bounded sample of the headline workload.  ``--measure-peaks`` times
@@ -76,6 +77,7 @@ def parse(argv=None):
     ap.add_argument("--tokens", type=int, default=0,
                     help="token rows per rank (default: the workload's own); smaller cases for profiler captures")
     ap.add_argument("--measure-peaks", action="store_true")
+    ap.add_argument("--details", metavar="FILE", help="write the full record of every layer to FILE (JSON)")
     ap.add_argument("--ref-seconds", type=float, default=120.0,
                     help="reference arm: CPU seconds for warm-up plus timed steps together")
     return ap.parse_args(argv)
@@ -618,6 +620,42 @@ def layer_result(L, args, t_step, t_k1, t_k2, clocks, dist, world, sms):
     }
 
 
+LINE_MAX = 2800   # characters: what keeps the end of a run's output keeps the whole line
+
+
+def _digits(v):
+    """Floats with nine significant digits, everywhere in a record."""
+    if isinstance(v, float):
+        return float(f"{v:.9g}")
+    if isinstance(v, dict):
+        return {k: _digits(x) for k, x in v.items()}
+    return [_digits(x) for x in v] if isinstance(v, (list, tuple)) else v
+
+
+def _pick(d, *keys):
+    return None if d is None else {k: d[k] for k in keys if k in d}
+
+
+def short_line(out):
+    """The printed line: the headline layer's figures without the notes on how
+    they are taken, and a row of figures for each of the other layers."""
+    s = {k: v for k, v in out.items() if not k.endswith("_note")}
+    s["kernels"] = {k: v for k, v in out["kernels"].items() if k != "timing"}
+    s["roofline"] = _pick(out["roofline"], "kernel", "bound", "achieved", "peak", "unit", "frac", "traffic")
+    s["e2e"] = _pick(out.get("e2e"), "value", "unit", "h2d_bytes_per_step", "d2h_bytes_per_step", "ms_per_step")
+    s["bf16_linear"] = _pick(out.get("bf16_linear"), "ms", "tflops")
+    s["clocks"] = _pick(out["clocks"], "sm_mhz", "sm_max_mhz", "reasons", "samples")
+    if "cpu_baseline" in out:
+        s["cpu_baseline"] = _pick(out["cpu_baseline"], "value", "unit", "cores", "kind")
+    if "configs" in out:
+        s["configs"] = {n: {"tokens_per_s": float(f"{r['tokens_per_s']:.4g}"),
+                            "us": [round(1e3 * r["ms_per_step"], 2), round(r["kernels"]["k1_rotate_quantize_us"], 2),
+                                   round(r["kernels"]["k2_gemm_us"], 2)],
+                            "k2_frac": round(r["kernels"]["k2_frac_peak"], 4)}
+                        for n, r in out["configs"].items()}
+    return _digits(s)
+
+
 def run_ours(args, names, rank, world, dist):
     import torch
 
@@ -645,6 +683,15 @@ def run_ours(args, names, rank, world, dist):
 
     if rank != 0:
         return
+    out = record(args, names, results, world)
+    if args.details:
+        with open(args.details, "w") as f:
+            json.dump(out, f, indent=1)
+    print(json.dumps(short_line(out)), flush=True)
+
+
+def record(args, names, results, world):
+    """Everything measured: the headline layer's figures on top, every layer's under `configs`."""
     head = results[HEADLINE] if HEADLINE in results else results[names[-1]]
     hw = inputs.workload(HEADLINE if HEADLINE in results else names[-1])
     out = {"metric": METRIC, "value": head["tokens_per_s"], "unit": "tokens/s", "n_gpus": world,
@@ -668,7 +715,7 @@ def run_ours(args, names, rank, world, dist):
                 if n != HEADLINE:
                     out["configs"][n]["cpu_baseline"] = cpu_baseline(inputs.workload(n), 3.0)
             out["configs"][HEADLINE]["cpu_baseline"] = out["cpu_baseline"]
-    print(json.dumps(out), flush=True)
+    return out
 
 
 # ----------------------------------------------------------------- peaks
