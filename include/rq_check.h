@@ -42,9 +42,10 @@ rq_status rq_convert_check(const float* in, int32_t n, uint8_t* e4m3, uint8_t* e
  * longer than the bound.
  * A kernel whose wait runs out records a code in the caller's status word
  * (rq_read_status then returns RQ_ERR_TIMEOUT), stops issuing copies and
- * MMAs (an MXFP4 product's MMAs within eight steps of 256 columns), waits
- * (bounded) for the ones already issued, frees its tensor memory and exits;
- * the outputs of that call are undefined.
+ * MMAs (an MXFP4 product's MMAs within eight steps of 256 columns, those of a
+ * one-launch layer with its last step, the 32nd at most), waits (bounded) for
+ * the ones already issued, frees its tensor memory and exits; the outputs of
+ * that call are undefined.
  */
 rq_status rq_set_wait_limit(uint64_t limit_ns, uint64_t* previous);
 
