@@ -394,7 +394,8 @@ rq_status rq_mxfp4_dequantize(int32_t rows, int32_t K, const uint8_t* codes, con
  *   [device, N x K/2], w_bscale from rq_quantize_weights(RQ_MXFP4, ...);
  *   Y [device, M x N] FP32 or BF16 (out_fp32).  M >= 0, K % 64 == 0,
  *   K <= 16384.
- *   At most 4 tokens with M K <= 16384 and K <= 8192 run in one launch.
+ *   At most 4 tokens with M K <= 16384, K <= 8192 and no more tiles of 128
+ *   outputs than the GPU has SMs (N <= 18944 on 148) run in one launch.
  *   workspace [device] at least rq_mxfp4_layer_workspace(M, N, K) bytes, its
  *   contents undefined before and after; calls that may overlap on the GPU
  *   need one each.  That function returns -1 for a shape outside the limits.

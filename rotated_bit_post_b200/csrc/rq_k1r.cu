@@ -733,7 +733,9 @@ cudaError_t launch_r_t64(const K1Launch& a, cudaStream_t st) {
 template <int BS>
 cudaError_t launch_r_t(const K1Launch& a, cudaStream_t st) {
   if (a.K % 128) return launch_r_t64<BS>(a, st);
-  // MXFP4 comes here for the double rotation; activations and weight rows alike
+  // MXFP4 comes here for the double rotation; activations and weight rows alike.
+  // 4096 x 1536: 22.7, 22.9, 21.2, 38.1 us with blocks of 16, 64, 128, 512.  Blocks
+  // of 16 to 64 spill 364 to 428 bytes, the others at most 32
   if (a.fmt == RQ_FMT_MXFP4) return launch_r<RQ_FMT_MXFP4, false, BS, 128>(a, st);
   if (a.weight) {
     switch (a.fmt) {

@@ -22,8 +22,9 @@
 //            the sum over a token's experts happens in the accumulator
 //
 // Bound by the bytes of the weights where there are many (64 tokens, 128 experts of
-// 2048 x 768, top 8: gate/up 40 us at 5 TB/s, down 25 us), by latencies where there are
-// few (1 x 4096 x 12288, fused: 10.9 us of which the weights' bytes are 4.1).
+// 2048 x 768, top 8: 82 us for the layer, of which 48 are the bytes; gate/up about
+// 40, down 25), by latencies where there are few (1 x 4096 x 12288, fused: 10.9 us
+// of which the weights' bytes are 4.1).
 //
 // Per CTA: warp 0 issues the copies (weights and tokens by TMA, 256 columns =
 // 128 bytes a row per stage; scale tiles by bulk copies), warp 1 moves the
@@ -544,9 +545,10 @@ cudaError_t launch_mode(const FewMaps& tm, FewParams p, int tiles, int ny, int s
     const int limit = (int64_t)tiles * ny * S > room ? 115712 : 230400;
     p.stages = (limit - FEW_TAIL - 1024 - x_bytes - rows_bytes - rot_bytes) / stage;
     // FUSED: beside long rows half an SM has room for few stages or none; fewer
-    // ranks with a whole SM each then (us for 1 x 6144 x 14336, blocks of 1024: 28.8 with
-    // two stages, 26.6 this way; 2 x 8192 x 18944, blocks of 512: 45.1 with one, 38.9;
-    // with three stages half an SM is as good or better: 4 x 4096 x 12288 24.6, 26.6)
+    // ranks with a whole SM each then (us with two stages in half an SM, and this way:
+    // 1 x 6144 x 14336, blocks of 1024: 17.5, 14.9; 4 x 4096 x 12288: 16.8, 16.0; with one
+    // stage, 2 x 8192 x 18900, blocks of 512: 29.9, 24.2; with three half an SM is as good
+    // or better: 3 x 4096 x 14336: 14.2, 14.5; 2 x 5120 x 11008: 13.9, 14.5)
     if (MODE != FUSED || S == 1 || p.stages >= FUSED_MIN_STAGES) break;
   }
   if (p.stages < 1) return cudaErrorInvalidValue;
@@ -616,8 +618,10 @@ cudaError_t launch_mx_few(const GemmLaunch& a, cudaStream_t st, const char** why
   return launch_mode<LINEAR>(tm, p, (a.N + 127) / 128, 1, (a.K + 255) / 256, a.num_sms > 0 ? a.num_sms : 148, st);
 }
 
-// The rows of a few tokens fit beside the weights' stages, and every CTA has an
-// SM to itself; the redundant transform is a few thousand values per CTA.
+// The rows of a few tokens fit beside the weights' stages, and there is an SM for
+// every tile of 128 outputs, so that a plan with one rank and a whole SM each always
+// exists; the redundant transform is a few thousand values per CTA.  Two CTAs of 384
+// threads per SM leave 80 registers, of which the transform's loops spill 60 bytes.
 bool mx_layer_fused(int M, int N, int K, int sms) {
   return M <= 4 && (int64_t)M * K <= 16384 && K <= 8192 && (N + 127) / 128 <= sms;
 }

@@ -11,10 +11,13 @@
 // is single: the epilogue brings it into registers as packed BF16 first, hands
 // it back, and stores while the next tile runs.
 //
-// 4608 x 12288 x 4096: 75 us, 6.2 PFLOP/s, tensor pipe 77% busy; a step of 256
-// columns takes 0.39 us, which is what its copies take without the MMAs (13 TB/s
-// from L2 over all SMs; the MMAs 0.27).  65520 x 1536 x 8960: 370-400 us, 0.8 of the
-// 3.2 us a tile between its last MMA and the next tile's first.
+// 4608 x 12288 x 4096: 75-77 us, 6.0-6.2 PFLOP/s, tensor pipe 77% busy (87 under the
+// power cap); a step of 256 columns takes 0.39 us, which is what its copies take
+// without the MMAs (13 TB/s from L2 over all SMs; the MMAs 0.27).  65520 x 1536 x
+// 8960: 370-400 us, 430-460 under the power cap, 0.8 of the 3.2 us a tile between
+// its last MMA and the next tile's first.  Below about 1000 tokens most SMs are idle:
+// K is not split, and 65 x 4096 x 4096 takes 16 pairs for 16 steps (10.4 us; the
+// layer 12.4, that of 64 tokens, in rq_mxfew.cu, 10.6).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

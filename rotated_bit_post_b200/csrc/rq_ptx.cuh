@@ -111,9 +111,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_
 
 // The same, reading the clock only after a second attempt (each may suspend the
 // thread for up to the hint's 1 ms): reading it takes about half a microsecond,
-// which a wait that ends meanwhile pays in full (an MXFP4 product of 4608 x 12288
-// x 4096: 110 us with mbar_wait, 95 with this; the grouped INT4 product, whose
-// many waiting warps share the issue slots, runs faster with mbar_wait: 68 against 77 us).
+// which a wait that ends meanwhile pays in full (an MXFP4 product of 32 x 8192 x
+// 12288: 14.0 us with mbar_wait, 13.7 with this; an expert layer of one token 18.5 and
+// 18.1; no difference at 4608 x 12288 x 4096.  The grouped INT4 product, whose many
+// waiting warps share the issue slots, runs faster with mbar_wait).
 // A barrier that is complete answers at once, and once another wait has run out
 // nothing is suspended any more: a loop that goes on after it ends in microseconds.
 __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, int32_t* status, int32_t code,
@@ -128,11 +129,11 @@ __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, i
 
 // ---------------------------------------------------------------- elected roles
 // A role that issues copies or MMAs is run by a whole warp, and elect_one() picks
-// the lane that issues; inside `if (lane == 0)` the compiler cannot see that
-// descriptors and addresses are one lane's, and wraps every tcgen05 instruction
-// in a loop over the lanes.  Measured, cycles for a step of four MMAs (N = 64)
-// and four scale copies, 225 by themselves: lane == 0: 752; a warp, descriptors
-// rebuilt per instruction: 548; a base plus the stage's offset: 385.
+// the lane that issues.  Measured, cycles for a step of four MMAs (N = 64) and four
+// scale copies, 225 by themselves: inside `if (lane == 0)`: 752; a warp with an
+// elected lane, descriptors rebuilt per instruction: 548; a base plus the stage's
+// offset: 385.  The cause is supposed, not shown: tcgen05 instructions want operands
+// that are the same for the whole warp, which a role of one lane hides.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
