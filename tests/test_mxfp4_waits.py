@@ -132,4 +132,3 @@ def test_long_product_ends_soon_after_a_wait_runs_out(L, M):
     _runs_out_then_recovers(call, [Y], st)
     # normal, expired, normal, expired, normal
     assert all(5.0 <= ms <= ENDS_WITHIN_MS for ms in took[1::2]), took
-    assert all(ms < 5.0 for ms in took[2::2]), took
